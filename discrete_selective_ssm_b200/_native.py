@@ -94,7 +94,13 @@ def lib(build_if_missing: bool = True):
             L.naju_testing_fwd_pieces.restype = i32
             L.naju_testing_bwd_pieces.argtypes = [vp]
             L.naju_testing_bwd_pieces.restype = i32
-            for name in ("naju_conv_silu_fwd", "naju_conv_silu_bwd", "naju_scan_fwd",
+            L.naju_vscan_workspace_bytes.argtypes = [dp]
+            L.naju_vscan_workspace_bytes.restype = sz
+            L.naju_vscan_fwd.argtypes = [dp] + [vp] * 8 + [sz, vp]
+            L.naju_vscan_bwd.argtypes = [dp] + [vp] * 12 + [sz, vp]
+            L.naju_vscan_step.argtypes = [i64, i64, i32] + [vp] * 7
+            for name in ("naju_vscan_fwd", "naju_vscan_bwd", "naju_vscan_step",
+                         "naju_conv_silu_fwd", "naju_conv_silu_bwd", "naju_scan_fwd",
                          "naju_scan_bwd", "naju_scan_step", "naju_conv_silu_step",
                          "naju_scan_step_conv", "naju_last_device_status"):
                 getattr(L, name).restype = ctypes.c_int
@@ -302,6 +308,125 @@ def scan_step_conv(state, conv_state, u, a, b, B, C, conv_w, conv_b=None, z=None
                                      _ptr(z, "z"), _ptr(D, "D", torch.float32),
                                      _ptr(state, "state", torch.float32), _ptr(y, "y"),
                                      _stream(stream)), "naju_scan_step_conv")
+    return y
+
+
+# ------------------------------------------------------- vector-state scan
+def _arg(t, name: str, shape, dtype, device):
+    """Data pointer of an argument that must be a contiguous `dtype` tensor of
+    `shape` on `device` (None passes through)."""
+    if t is None:
+        return None
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _launch(device, stream, call, where: str):
+    """call(raw stream) with `device` current; `stream` defaults to that
+    device's current one."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        _check(call(raw), where)
+    else:
+        with torch.cuda.device(device):
+            _check(call(raw), where)
+
+
+def _vdims(h, out_dtype) -> Dims:
+    if h.dim() != 3:
+        raise ValueError(f"h must be [batch, seqlen, d_inner], got {tuple(h.shape)}")
+    if not h.is_cuda:
+        raise ValueError("h must be a CUDA tensor")
+    Bt, L, d = h.shape
+    return make_dims(Bt, L, d, 1, _dt(h), out_dtype, 0)
+
+
+def vscan_workspace(dims: Dims, device) -> torch.Tensor:
+    """A workspace of vscan_fwd and vscan_bwd (contents undefined)."""
+    n = int(lib().naju_vscan_workspace_bytes(ctypes.byref(dims)))
+    if n == 0:
+        raise NajuError(1, "naju_vscan_workspace_bytes")
+    ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
+    off = (-ws.data_ptr()) % 256
+    return ws[off:off + n]
+
+
+def _ws_arg(ws, device):
+    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    return ws.data_ptr()
+
+
+def vscan_fwd(h, a, b=None, *, z=None, x0=None, out_dtype=None, workspace=None, want_final=True,
+              y=None, x_final=None, stream=None):
+    """Vector-state scan over [batch, seqlen, d_inner]: x_t = f x_{t-1} + i h,
+    y = x SiLU(z).  b None: coupled gate; z None: no modulation.  Returns
+    (y, x_final, workspace); the workspace is what vscan_bwd needs."""
+    dims = _vdims(h, out_dtype)
+    dev, dt, act, st = h.device, h.dtype, h.shape, (h.shape[0], h.shape[2])
+    if workspace is None:
+        workspace = vscan_workspace(dims, dev)
+    ot = _torch_dt(dims.out_dtype)
+    if y is None:
+        y = torch.empty(act, dtype=ot, device=dev)
+    if x_final is None and want_final:
+        x_final = torch.empty(st, dtype=torch.float32, device=dev)
+    f32, L = torch.float32, lib()
+    args = (ctypes.byref(dims), _arg(h, "h", act, dt, dev), _arg(a, "a", act, dt, dev),
+            _arg(b, "b", act, dt, dev), _arg(z, "z", act, dt, dev), _arg(x0, "x0", st, f32, dev),
+            _arg(y, "y", act, ot, dev), _arg(x_final, "x_final", st, f32, dev),
+            _ws_arg(workspace, dev), workspace.numel())
+    _launch(dev, stream, lambda s: L.naju_vscan_fwd(*args, s), "naju_vscan_fwd")
+    return y, x_final, workspace
+
+
+def vscan_bwd(dy, h, a, b, workspace, *, z=None, dx_final=None, out_dtype=None, want_dx0=True,
+              grads=None, stream=None):
+    """Gradients of vscan_fwd; `workspace` must hold that forward's
+    checkpoints.  Returns a dict: dh, da, db (None without b), dz (None
+    without z), dx0 (None unless wanted)."""
+    dims = _vdims(h, out_dtype)
+    dev, dt, act, st = h.device, h.dtype, h.shape, (h.shape[0], h.shape[2])
+    ot, f32 = _torch_dt(dims.out_dtype), torch.float32
+    if grads is None:
+        new = lambda want=True: torch.empty(act, dtype=ot, device=dev) if want else None  # noqa: E731
+        grads = {"dh": new(), "da": new(), "db": new(b is not None), "dz": new(z is not None),
+                 "dx0": torch.empty(st, dtype=f32, device=dev) if want_dx0 else None}
+    g = grads
+    L = lib()
+    args = (ctypes.byref(dims), _arg(h, "h", act, dt, dev), _arg(a, "a", act, dt, dev),
+            _arg(b, "b", act, dt, dev), _arg(z, "z", act, dt, dev),
+            _arg(dy, "dy", act, dt, dev), _arg(dx_final, "dx_final", st, f32, dev),
+            _arg(g["dh"], "dh", act, ot, dev), _arg(g["da"], "da", act, ot, dev),
+            _arg(g.get("db"), "db", act, ot, dev), _arg(g.get("dz"), "dz", act, ot, dev),
+            _arg(g.get("dx0"), "dx0", st, f32, dev), _ws_arg(workspace, dev), workspace.numel())
+    _launch(dev, stream, lambda s: L.naju_vscan_bwd(*args, s), "naju_vscan_bwd")
+    return g
+
+
+def vscan_step(state, h, a, b=None, z=None, y=None, stream=None):
+    """One decode step of the vector-state scan: h, a, b, z [batch, d_inner];
+    `state` [batch, d_inner] fp32 is updated in place.  Returns y."""
+    if h.dim() != 2:
+        raise ValueError(f"h must be [batch, d_inner], got {tuple(h.shape)}")
+    dev, dt, sh = h.device, h.dtype, h.shape
+    if y is None:
+        y = torch.empty_like(h)
+    L = lib()
+    args = (sh[0], sh[1], _dt(h), _arg(h, "h", sh, dt, dev), _arg(a, "a", sh, dt, dev),
+            _arg(b, "b", sh, dt, dev), _arg(z, "z", sh, dt, dev),
+            _arg(state, "state", sh, torch.float32, dev), _arg(y, "y", sh, dt, dev))
+    _launch(dev, stream, lambda s: L.naju_vscan_step(*args, s), "naju_vscan_step")
     return y
 
 

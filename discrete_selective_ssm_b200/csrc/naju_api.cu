@@ -248,6 +248,36 @@ Layout layout(const naju_dims* dm) {
     return l;
 }
 
+// Vector-state scan: workspace layout (status word; forward ticket and flags;
+// backward ticket and flags; item aggregates; checkpoints; adjoints).
+struct VLayout {
+    int64_t ntiles, units, nk;
+    size_t off_fsync, off_bsync, sync_bytes, off_agg, off_ckpt, off_adj, total;
+};
+constexpr size_t kTicketBytes = 128;
+VLayout vlayout(const naju_dims* dm) {
+    VLayout l{};
+    const int64_t tile = vscan_tile(dm->dtype);
+    l.ntiles = cdiv(dm->d_inner, tile);
+    l.units = dm->batch * l.ntiles;
+    l.nk = cdiv(dm->seqlen, vscan_tokens());
+    const size_t items = (size_t)l.units * l.nk;
+    l.sync_bytes = l.nk > 1 ? kTicketBytes + sizeof(int) * items : 0;
+    size_t off = 256;
+    l.off_fsync = off;
+    off = up256(off + l.sync_bytes);
+    l.off_bsync = off;
+    off = up256(off + l.sync_bytes);
+    l.off_agg = off;
+    off = up256(off + (l.nk > 1 ? sizeof(float2) * items * tile : 0));
+    l.off_ckpt = off;
+    off = up256(off + sizeof(float) * items * tile);
+    l.off_adj = off;
+    off = up256(off + (l.nk > 1 ? sizeof(float) * items * tile : 0));
+    l.total = off;
+    return l;
+}
+
 inline naju_status cuda_status(cudaError_t e) { return e == cudaSuccess ? NAJU_OK : NAJU_ERR_CUDA; }
 
 #define NAJU_REQUIRE(cond) \
@@ -278,6 +308,35 @@ naju_status check_dims(const naju_dims* dm) {
 }
 
 }  // namespace naju
+
+namespace {
+
+// Dims of the vector-state scan: the sequence checks with d_state 1, and a
+// work-item count that fits the ticket.
+naju_status check_vdims(const naju_dims* dm) {
+    if (!dm) return NAJU_ERR_INVALID_ARG;
+    naju_dims m = *dm;
+    if (m.d_state == 1) m.d_state = 16;  // the sequence checks' own smallest
+    else return NAJU_ERR_UNSUPPORTED;
+    const naju_status st = check_dims(&m);
+    if (st != NAJU_OK) return st;
+    const int64_t items = dm->batch * cdiv(dm->d_inner, vscan_tile(dm->dtype)) *
+                          cdiv(dm->seqlen, vscan_tokens());
+    return items < (1LL << 31) - 1 ? NAJU_OK : NAJU_ERR_INVALID_ARG;
+}
+
+void vscan_params(VscanParams& p, const naju_dims* dims, const VLayout& l, char* ws) {
+    p.status = reinterpret_cast<int*>(ws);
+    p.agg = reinterpret_cast<float2*>(ws + l.off_agg);
+    p.ckpt = reinterpret_cast<float*>(ws + l.off_ckpt);
+    p.adj = reinterpret_cast<float*>(ws + l.off_adj);
+    p.L = dims->seqlen; p.d = dims->d_inner;
+    p.units = l.units; p.nk = l.nk; p.ntiles = (int)l.ntiles;
+    p.wait_limit = g_wait_limit;
+    p.fault_skip_publish = g_skip_publish;
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -456,6 +515,71 @@ naju_status naju_scan_step_conv(int64_t batch, int64_t d_inner, int64_t d_state,
     return cuda_status(launch_scan_step(batch, d_inner, d_state, u, a, b, B, C, z, D, state, y,
                                         dtype, conv_w, conv_b, conv_state,
                                         static_cast<cudaStream_t>(stream)));
+}
+
+size_t naju_vscan_workspace_bytes(const naju_dims* dims) {
+    if (check_vdims(dims) != NAJU_OK) return 0;
+    return vlayout(dims).total;
+}
+
+naju_status naju_vscan_fwd(const naju_dims* dims, const void* h, const void* a, const void* b,
+                           const void* z, const float* x0, void* y, float* x_final,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+    const naju_status st = check_vdims(dims);
+    if (st != NAJU_OK) return st;
+    NAJU_REQUIRE(ok_act(h) && ok_act(a) && ok_opt(b) && ok_opt(z) && ok_act(y));
+    NAJU_REQUIRE(ok_opt(x0) && ok_opt(x_final));
+    NAJU_REQUIRE(workspace && aligned(workspace, 256));
+    const VLayout l = vlayout(dims);
+    NAJU_REQUIRE(workspace_bytes >= l.total);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    // status, ticket and flags in one go (one item per unit needs none of
+    // them: the kernel clears the status word itself)
+    if (l.nk > 1 && cudaMemsetAsync(ws, 0, l.off_fsync + l.sync_bytes, s) != cudaSuccess)
+        return NAJU_ERR_CUDA;
+    VscanParams p{};
+    vscan_params(p, dims, l, ws);
+    p.h = h; p.a = a; p.b = b; p.z = z; p.x0 = x0; p.y = y; p.x_final = x_final;
+    p.ticket = reinterpret_cast<int*>(ws + l.off_fsync);
+    p.flags = reinterpret_cast<int*>(ws + l.off_fsync + kTicketBytes);
+    return cuda_status(launch_vscan_fwd(p, dims->dtype, dims->out_dtype, s));
+}
+
+naju_status naju_vscan_bwd(const naju_dims* dims, const void* h, const void* a, const void* b,
+                           const void* z, const void* dy, const float* dx_final, void* dh,
+                           void* da, void* db, void* dz, float* dx0, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    const naju_status st = check_vdims(dims);
+    if (st != NAJU_OK) return st;
+    NAJU_REQUIRE(ok_act(h) && ok_act(a) && ok_opt(b) && ok_opt(z) && ok_act(dy));
+    NAJU_REQUIRE(ok_act(dh) && ok_act(da) && (!b || ok_act(db)) && (!z || ok_act(dz)));
+    NAJU_REQUIRE(ok_opt(dx_final) && ok_opt(dx0));
+    NAJU_REQUIRE(workspace && aligned(workspace, 256));
+    const VLayout l = vlayout(dims);
+    NAJU_REQUIRE(workspace_bytes >= l.total);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    if (l.nk > 1 && cudaMemsetAsync(ws + l.off_bsync, 0, l.sync_bytes, s) != cudaSuccess)
+        return NAJU_ERR_CUDA;
+    VscanParams p{};
+    vscan_params(p, dims, l, ws);
+    p.h = h; p.a = a; p.b = b; p.z = z; p.dy = dy; p.dx_final = dx_final;
+    p.dh = dh; p.da = da; p.db = db; p.dz = dz; p.dx0 = dx0;
+    p.ticket = reinterpret_cast<int*>(ws + l.off_bsync);
+    p.flags = reinterpret_cast<int*>(ws + l.off_bsync + kTicketBytes);
+    return cuda_status(launch_vscan_bwd(p, dims->dtype, dims->out_dtype, s));
+}
+
+naju_status naju_vscan_step(int64_t batch, int64_t d_inner, int32_t dtype, const void* h,
+                            const void* a, const void* b, const void* z, float* state, void* y,
+                            void* stream) {
+    if (batch < 1 || d_inner < 1 || batch > (1 << 20) || d_inner > (1 << 20))
+        return NAJU_ERR_INVALID_ARG;
+    if (dtype != NAJU_F32 && dtype != NAJU_BF16) return NAJU_ERR_UNSUPPORTED;
+    NAJU_REQUIRE(ok_act(h) && ok_act(a) && ok_opt(b) && ok_opt(z) && ok_act(state) && ok_act(y));
+    return cuda_status(launch_vscan_step(batch * d_inner, h, a, b, z, state, y, dtype,
+                                         static_cast<cudaStream_t>(stream)));
 }
 
 naju_status naju_last_device_status(void* workspace, void* stream) {

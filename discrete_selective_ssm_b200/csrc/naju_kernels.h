@@ -134,4 +134,39 @@ cudaError_t launch_conv_step(int64_t Bt, int64_t d, const void* u, const float* 
                              const float* bias, float* conv_state, void* h, int dtype,
                              cudaStream_t st);
 
+// ------------------------------------------------------ vector-state scan
+struct VscanParams {
+    const void* h;
+    const void* a;
+    const void* b;          // null: coupled gate i = 1 - f
+    const void* z;          // null: no modulation
+    const float* x0;        // forward; null: zero
+    const void* dy;         // backward
+    const float* dx_final;  // backward; null: zero
+    void* y;
+    float* x_final;         // may be null
+    void* dh;
+    void* da;
+    void* db;
+    void* dz;
+    float* dx0;             // may be null
+    int* status;
+    int* ticket;            // cleared before the launch, followed by the flags
+    int* flags;             // [units][nk]
+    float2* agg;            // [units][nk][tile]: an item's (P, X), backward (P, R)
+    float* ckpt;            // [units][nk][tile]: state entering each item
+    float* adj;             // [units][nk][tile]: adjoint leaving each item (backward)
+    int64_t L, d;
+    int64_t units, nk;      // batch * channel tiles; items per unit
+    int ntiles;
+    long long wait_limit;
+    int fault_skip_publish;
+};
+int vscan_tile(int dtype);  // channels per item
+int vscan_tokens();         // tokens per item
+cudaError_t launch_vscan_fwd(const VscanParams& p, int dtype, int out_dtype, cudaStream_t st);
+cudaError_t launch_vscan_bwd(const VscanParams& p, int dtype, int out_dtype, cudaStream_t st);
+cudaError_t launch_vscan_step(int64_t n, const void* h, const void* a, const void* b,
+                              const void* z, float* state, void* y, int dtype, cudaStream_t st);
+
 }  // namespace naju

@@ -181,6 +181,44 @@ naju_status naju_scan_step_conv(int64_t batch, int64_t d_inner, int64_t d_state,
                                 const void* C, const void* z, const float* D, float* state,
                                 void* y, void* stream);
 
+/* ---- Vector-state scan: the recurrence with one state value per channel
+ * (no B and C), for layers that keep a [batch, d_inner] state:
+ *   x_t = f_t x_{t-1} + i_t h_t,   f = sigmoid(a), i = sigmoid(b),
+ *   y_t = x_t SiLU(z_t).
+ * dims->d_state must be 1 (UNSUPPORTED otherwise); conv_width is not read.
+ * b == NULL selects the coupled gate i = 1 - f, z == NULL no modulation.
+ * The gates saturate exactly: a = -inf starts a sequence afresh at that token
+ * (packed documents), a = +inf with b = -inf leaves the state as it is
+ * (padding); h and z must be finite there.  Results do not depend on how the
+ * work was scheduled: two calls on the same inputs agree bit for bit. */
+
+/* Workspace of naju_vscan_fwd / naju_vscan_bwd, under the rules of
+ * naju_scan_workspace_bytes; it need not be cleared.  0 if dims are invalid. */
+size_t naju_vscan_workspace_bytes(const naju_dims* dims);
+
+/* Forward over [batch, seqlen, d_inner].  x0 and x_final are [batch, d_inner]
+ * fp32; x0 == NULL means zero, x_final may be NULL.  Clears the workspace's
+ * status word and writes the checkpoints that the backward reads. */
+naju_status naju_vscan_fwd(const naju_dims* dims, const void* h, const void* a, const void* b,
+                           const void* z, const float* x0, void* y, float* x_final,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward of naju_vscan_fwd for a loss with gradient dy (dtype) w.r.t. y and,
+ * optionally, dx_final [batch, d_inner] fp32 w.r.t. x_final.  Same inputs as
+ * the forward, whose workspace it reads (the initial state comes from there).
+ * Writes dh, da, db (with b), dz (with z) in out_dtype and dx0 (fp32, may be
+ * NULL).  With b == NULL da includes the write-gate path. */
+naju_status naju_vscan_bwd(const naju_dims* dims, const void* h, const void* a, const void* b,
+                           const void* z, const void* dy, const float* dx_final, void* dh,
+                           void* da, void* db, void* dz, float* dx0, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* One decode step: h, a, b, z, y are [batch, d_inner] in `dtype`; state
+ * [batch, d_inner] fp32 is updated in place.  Uses no workspace. */
+naju_status naju_vscan_step(int64_t batch, int64_t d_inner, int32_t dtype, const void* h,
+                            const void* a, const void* b, const void* z, float* state, void* y,
+                            void* stream);
+
 /* Synchronises `stream`, reads the workspace's status word (NAJU_OK or
  * NAJU_ERR_TIMEOUT) and clears it.  Returns NAJU_ERR_CUDA if the stream
  * itself reports an error. */

@@ -1,0 +1,329 @@
+"""The vector-state scan (forward, backward, decode step) against the fp64
+definition in vscan_ref.
+
+Bounds, element by element.  Every operation of the kernels rounds by at most
+half a step (u = 2^-24 relative); a gate value is off by at most 6 u of itself
+(base-2 exponential 2 steps, its argument, the sum, the reciprocal), times a
+further |logit| u where it is the small one.  A term of x_t passes at most
+t + 1 gates and additions, so x_t is off by at most 8 u (t + 8) of the same
+recurrence over |h| and |x0|; a gradient is such a product of a forward and a
+reverse recurrence: 8 u (L + 16 + max|logit|) of the gradient formed of absolute
+values.  bf16 outputs add half a bf16 step, 2^-8 of the value.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import discrete_selective_ssm_b200 as naju
+import vscan_ref as ref
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def make(Bt, L, d, dtype="f32", coupled=False, z=True, x0=True, seed=0, a=(5.0, 1.0),
+         b=(-2.0, 1.0)):
+    g = torch.Generator().manual_seed(1000 + seed)
+
+    def rn(shape, mean=0.0, std=1.0, dt=DT[dtype]):
+        return (torch.randn(shape, generator=g) * std + mean).to(dt).cuda()
+
+    act = (Bt, L, d)
+    return {"h": rn(act), "a": rn(act, *a), "b": None if coupled else rn(act, *b),
+            "z": rn(act) if z else None, "dy": rn(act),
+            "x0": rn((Bt, d), dt=torch.float32) if x0 else None,
+            "dx_final": rn((Bt, d), dt=torch.float32) if x0 else None}
+
+
+def bounds(t):
+    """Sums of absolute values: (y, x_final) and the gradients."""
+    ab = lambda v: None if v is None else v.double().abs()  # noqa: E731
+    h, a, b, z, x0, dy, dxf = (t[k] for k in ("h", "a", "b", "z", "x0", "dy", "dx_final"))
+    _, xf, xs = ref.fwd(ab(h), a, b, None, ab(x0))
+    av, zv = ref.f64(a), ref.f64(z)
+    f, fc = ref.sigmoid(av), ref.sigmoid(-av)
+    i = fc if b is None else ref.sigmoid(ref.f64(b))
+    ic = None if b is None else ref.sigmoid(-ref.f64(b))
+    y, dyv, out = xs[:, 1:], np.abs(ref.f64(dy)), {}
+    dx = dyv
+    if z is not None:
+        s = ref.sigmoid(zv)
+        y = y * np.abs(zv) * s
+        out["dz"] = dyv * xs[:, 1:] * (s + np.abs(zv) * s * (1 - s))
+        dx = dyv * np.abs(zv) * s
+    g = np.zeros_like(dx)
+    r = np.zeros_like(xf) if dxf is None else np.abs(ref.f64(dxf))
+    for k in range(dx.shape[1] - 1, -1, -1):
+        g[:, k] = dx[:, k] + r
+        r = f[:, k] * g[:, k]
+    hv = np.abs(ref.f64(h))
+    out["dx0"], out["dh"] = r, g * i
+    out["da"] = g * (xs[:, :-1] + (hv if b is None else 0.0)) * f * fc
+    if b is not None:
+        out["db"] = g * hv * i * ic
+    return y, xf, out
+
+
+def factor(t):
+    m = max(float(t[k].float().nan_to_num(posinf=0, neginf=0).abs().max())
+            for k in ("a", "b", "z") if t[k] is not None)
+    return 8 * U * (t["h"].shape[1] + 16 + m)
+
+
+def near(got, want, allow, name):
+    g = ref.f64(got)
+    assert g.shape == want.shape, name
+    assert np.all(np.isfinite(g)), f"{name}: non-finite values"
+    if got.dtype == torch.bfloat16:
+        allow = allow + 2.0 ** -8 * np.abs(want)
+    over = np.abs(g - want) - allow - 1e-30
+    k = np.unravel_index(np.argmax(over), over.shape)
+    assert over[k] <= 0, f"{name} at {k}: got {g[k]!r}, want {want[k]!r}, allowed {allow[k]:.3e}"
+
+
+def run(t, out_dtype=None, **kw):
+    y, xf, ws = naju.vscan_fwd(t["h"], t["a"], t["b"], z=t["z"], x0=t["x0"],
+                               out_dtype=out_dtype, **kw)
+    g = naju.vscan_bwd(t["dy"], t["h"], t["a"], t["b"], ws, z=t["z"], dx_final=t["dx_final"],
+                       out_dtype=out_dtype)
+    assert naju.last_device_status(ws) == 0
+    return y, xf, g
+
+
+def check(t, out_dtype=None):
+    y, xf, g = run(t, out_dtype)
+    ry, rx, _ = ref.fwd(t["h"], t["a"], t["b"], t["z"], t["x0"])
+    rg = ref.bwd(t["dy"], t["h"], t["a"], t["b"], t["z"], t["x0"], t["dx_final"])
+    by, bx, bg = bounds(t)
+    k = factor(t)
+    near(y, ry, k * by, "y")
+    near(xf, rx, k * bx, "x_final")
+    for n in ("dh", "da", "db", "dz", "dx0"):
+        assert (g[n] is None) == (rg[n] is None), n
+        if g[n] is not None:
+            near(g[n], rg[n], 2 * k * bg[n], n)
+    return y, xf, g
+
+
+@pytest.mark.parametrize("coupled", [False, True])
+@pytest.mark.parametrize("z", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_parity(dtype, z, coupled):
+    check(make(2, 300, 200, dtype, coupled, z), naju.F32)
+
+
+@pytest.mark.parametrize("L", [1, 2, 7, 8, 63, 64, 65, 127, 129, 640])
+@pytest.mark.parametrize("d", [1, 63, 64, 130])
+def test_lengths_and_widths(L, d):
+    check(make(3, L, d, "bf16", seed=L + d))
+
+
+@pytest.mark.parametrize("d", [1, 31, 32, 33, 100])
+def test_widths_f32(d):
+    check(make(2, 97, d, "f32", coupled=True, seed=d))
+
+
+def test_no_initial_state_and_no_final_gradient():
+    check(make(2, 130, 48, "f32", x0=False))
+
+
+def test_one_long_sequence():
+    """Many items of one unit: the look-back spans more than its window."""
+    check(make(1, 20000, 40, "f32", seed=9))
+
+
+def test_long_memory():
+    """f within 1e-4 of one: the state sums thousands of tokens."""
+    check(make(2, 3000, 32, "f32", seed=3, a=(9.0, 0.5)))
+
+
+def test_saturated_gates():
+    """Logits far out on both sides: neither gate loses its small part."""
+    check(make(2, 200, 64, "f32", seed=4, a=(0.0, 12.0), b=(0.0, 12.0)))
+    check(make(2, 200, 64, "f32", seed=4, a=(0.0, 12.0), coupled=True))
+    check(make(2, 200, 64, "bf16", seed=4, a=(0.0, 30.0), b=(0.0, 30.0)))
+
+
+def lowest(dt):
+    return torch.finfo(dt).min
+
+
+@pytest.mark.parametrize("far", ["inf", "lowest"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_packed_and_padded(dtype, far):
+    """a = -inf starts afresh: the documents of a packed row equal their own
+    runs, and no gradient crosses.  a = +inf, b = -inf keeps the state."""
+    big = math.inf if far == "inf" else -lowest(DT[dtype])
+    t = make(1, 150, 64, dtype, x0=False, seed=6)
+    cut = 70
+    t["a"][:, cut] = -big
+    y, xf, g = run(t)
+    s = {k: None if v is None else v[:, cut:].contiguous() for k, v in t.items()}
+    y2, xf2, g2 = run(s)
+    ab, bb = t["a"].clone(), t["b"].clone()
+    ab[:, cut] = -700.0  # the definition's e^{-a} stays finite there
+    ry, rx, _ = ref.fwd(t["h"], ab, t["b"], t["z"], None)
+    by, bx, _ = bounds({**t, "a": ab})
+    near(y, ry, factor(t) * by, "y")
+    near(y2, ry[:, cut:], factor(t) * by[:, cut:], "own run")
+    assert float(g["da"][:, cut].abs().max()) == 0.0
+    for n in ("dh", "da", "db", "dz"):
+        near(g[n][:, cut:], ref.f64(g2[n]), 2 ** -7 * np.abs(ref.f64(g2[n])) + 1e-5, n)
+    p = make(2, 100, 64, dtype, seed=7)
+    q = {k: None if v is None else v[:, :60].contiguous() if v.dim() == 3 else v
+         for k, v in p.items()}
+    p["a"][:, 60:] = big
+    p["b"][:, 60:] = -big
+    p["dy"][:, 60:] = 0
+    y, xf, g = run(p)
+    y2, xf2, g2 = run(q)
+    assert torch.equal(y[:, :60], y2)
+    assert float(g["db"][:, 60:].abs().max()) == 0.0 and float(g["da"][:, 60:].abs().max()) == 0.0
+    _, rx, _ = ref.fwd(q["h"], q["a"], q["b"], None, q["x0"])
+    _, bx, bg = bounds(q)
+    near(xf, rx, factor(p) * bx, "x_final")
+    near(g["dx0"], ref.bwd(q["dy"], q["h"], q["a"], q["b"], q["z"], q["x0"],
+                           q["dx_final"])["dx0"], 2 * factor(p) * bg["dx0"], "dx0")
+
+
+def test_nan_logit_stays():
+    t = make(1, 80, 64, "f32", x0=False)
+    t["a"][0, 10, 3] = math.nan
+    y, xf, _ = naju.vscan_fwd(t["h"], t["a"], t["b"], z=t["z"])
+    assert torch.isnan(y[0, 10:, 3]).all() and torch.isnan(xf[0, 3])
+    assert torch.isfinite(y[0, :10]).all() and torch.isfinite(y[0, :, :3]).all()
+
+
+def test_gradients_against_differences():
+    t = make(1, 90, 33, "f32", seed=8)
+    _, _, g = run(t)
+
+    def loss(s):
+        y, xf, _ = ref.fwd(s["h"], s["a"], s["b"], s["z"], s["x0"])
+        return float((y * ref.f64(t["dy"])).sum() + (xf * ref.f64(t["dx_final"])).sum())
+
+    for k, n in (("h", "dh"), ("a", "da"), ("b", "db"), ("z", "dz"), ("x0", "dx0")):
+        v = torch.randn(t[k].shape, generator=torch.Generator().manual_seed(5)).double()
+        e = 1e-5
+        hi = loss({**t, k: t[k].double().cpu() + e * v})
+        lo = loss({**t, k: t[k].double().cpu() - e * v})
+        got = float((g[n].double().cpu() * v).sum())
+        size = float((g[n].double().cpu() * v).abs().sum())
+        # fp32 gradients (8 u (L + 16) of their terms) and the difference's e^2
+        assert abs(got - (hi - lo) / (2 * e)) <= 1e-4 * size, n
+
+
+def test_bitwise_repeatable():
+    """The order in which items finish never changes a result."""
+    t = make(2, 9000, 256, "f32", seed=11)
+    first = run(t)
+    for _ in range(5):
+        again = run(t)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+        for n in ("dh", "da", "db", "dz", "dx0"):
+            assert torch.equal(first[2][n], again[2][n]), n
+
+
+def test_steps_equal_the_forward():
+    t = make(3, 70, 129, "f32", seed=12)
+    state = t["x0"].clone()
+    ys = [naju.vscan_step(state, *(t[k][:, i].contiguous() for k in ("h", "a", "b", "z")))
+          for i in range(70)]
+    ry, rx, _ = ref.fwd(t["h"], t["a"], t["b"], t["z"], t["x0"])
+    by, bx, _ = bounds(t)
+    near(torch.stack(ys, 1), ry, factor(t) * by, "y")
+    near(state, rx, factor(t) * bx, "state")
+
+
+@pytest.mark.parametrize("Bt,d", [(1, 1), (1, 7), (5, 13), (256, 2048), (3, 1000)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("coupled", [False, True])
+def test_step(Bt, d, dtype, coupled):
+    t = make(Bt, 1, d, dtype, coupled, z=not coupled, seed=d)
+    one = {k: None if v is None else v.view(Bt, d) for k, v in t.items()}
+    state = one["x0"].clone()
+    y = naju.vscan_step(state, one["h"], one["a"], one["b"], one["z"])
+    ry, rx, _ = ref.fwd(t["h"], t["a"], t["b"], t["z"], t["x0"])
+    by, bx, _ = bounds(t)
+    near(y, ry[:, 0], factor(t) * by[:, 0], "y")
+    near(state, rx, factor(t) * bx, "state")
+
+
+def test_outputs_stay_inside_their_tensors():
+    """Neighbours of every output keep their values (odd width, ragged end)."""
+    t = make(1, 67, 33, "bf16", seed=13)
+    n = 67 * 33
+    bufs = {k: torch.full((n + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+            for k in ("y", "dh", "da", "db", "dz")}
+    view = {k: v[:n].view(1, 67, 33) for k, v in bufs.items()}
+    y, _, ws = naju.vscan_fwd(t["h"], t["a"], t["b"], z=t["z"], x0=t["x0"], y=view["y"])
+    g = {k: view[k] for k in ("dh", "da", "db", "dz")}
+    naju.vscan_bwd(t["dy"], t["h"], t["a"], t["b"], ws, z=t["z"], grads=g)
+    torch.cuda.synchronize()
+    for k, v in bufs.items():
+        assert bool((v[n:] == 7.0).all()), k
+
+
+def test_another_stream_and_a_graph():
+    """On a side stream, and captured (forward and backward together) and
+    replayed on new inputs while eager results live."""
+    t, s = make(2, 500, 64, "f32", seed=14), make(2, 500, 64, "f32", seed=15)
+    want = run(s)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = run(s)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2]["da"], want[2]["da"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, xf, ws = naju.vscan_fwd(t["h"], t["a"], t["b"], z=t["z"], x0=t["x0"])
+        g = naju.vscan_bwd(t["dy"], t["h"], t["a"], t["b"], ws, z=t["z"],
+                           dx_final=t["dx_final"])
+    for k in t:
+        t[k].copy_(s[k])
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[0]) and torch.equal(xf, want[1])
+    for n in ("dh", "da", "db", "dz", "dx0"):
+        assert torch.equal(g[n], want[2][n]), n
+
+
+def test_bounded_wait_reports():
+    """An item that never publishes its state: the waits run out, the call
+    returns, and the next call is right."""
+    t = make(1, 300, 32, "f32", seed=16)
+    naju.testing_set_wait_limit(200)
+    naju.testing_set_skip_publish(True)
+    try:
+        _, _, ws = naju.vscan_fwd(t["h"], t["a"], t["b"])
+        assert naju.last_device_status(ws) == 4
+        assert naju.last_device_status(ws) == 0
+        naju.vscan_bwd(t["dy"], t["h"], t["a"], t["b"], ws)
+        assert naju.last_device_status(ws) == 4
+    finally:
+        naju.testing_set_wait_limit(0)
+        naju.testing_set_skip_publish(False)
+    check(t)
+
+
+def test_refusals_on_device_tensors():
+    t = make(1, 10, 32, "f32")
+    with pytest.raises(ValueError):
+        naju.vscan_fwd(t["h"], t["a"][:, :9])
+    with pytest.raises(TypeError):
+        naju.vscan_fwd(t["h"], t["a"].bfloat16())
+    with pytest.raises(ValueError):
+        naju.vscan_fwd(t["h"].transpose(1, 2).contiguous().transpose(1, 2), t["a"])
+    with pytest.raises(naju.NajuError):
+        naju.vscan_fwd(t["h"][:, :0], t["a"][:, :0])
+    with pytest.raises(naju.NajuError):
+        naju.vscan_fwd(t["h"], t["a"], out_dtype=naju.BF16)
+    with pytest.raises(naju.NajuError):
+        naju.vscan_fwd(t["h"], t["a"], workspace=torch.empty(256, dtype=torch.uint8,
+                                                             device="cuda"))
