@@ -38,7 +38,8 @@ def sources():
 
 
 def _headers():
-    return glob.glob(os.path.join(CSRC, "*.h*")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return [f for d, pat in ((CSRC, "*.h*"), (CSRC, "*.cuh"), (INCLUDE, "*.h"))
+            for f in glob.glob(os.path.join(d, pat))]
 
 
 def _stale() -> bool:
