@@ -27,6 +27,7 @@ int g_bwd_pieces = 0;  // 0 automatic, < 0 never, > 0 that many ranges
 int g_fwd_pieces = 0;  // the same for the tensor-core forward
 int g_fwd_impl = 0;  // 0 automatic, 1 CUDA cores, 2 tensor-core sub-chunk, 3 block form
 int g_bwd_impl = 0;  // 0 automatic, 1 CUDA cores, 2 tensor-core sub-chunk, 3 block form
+int g_vcluster = 0;  // > 0: blocks per unit of the vector-state scan
 int g_sm_override = 0;  // > 0: SM count used by the tiling (tests)
 
 // Streaming multiprocessors of the current device, queried once per device
@@ -248,34 +249,30 @@ Layout layout(const naju_dims* dm) {
     return l;
 }
 
-// Vector-state scan: workspace layout (status word; forward ticket and flags;
-// backward ticket and flags; item aggregates; checkpoints; adjoints).
+// Vector-state scan: workspace layout (status word, checkpoints).
 struct VLayout {
-    int64_t ntiles, units, nk;
-    size_t off_fsync, off_bsync, sync_bytes, off_agg, off_ckpt, off_adj, total;
+    int64_t ntiles, units, nkf, nkb;  // items per unit, forward and backward
+    size_t off_ckpt, total;
 };
-constexpr size_t kTicketBytes = 128;
 VLayout vlayout(const naju_dims* dm) {
     VLayout l{};
     const int64_t tile = vscan_tile(dm->dtype);
     l.ntiles = cdiv(dm->d_inner, tile);
     l.units = dm->batch * l.ntiles;
-    l.nk = cdiv(dm->seqlen, vscan_tokens());
-    const size_t items = (size_t)l.units * l.nk;
-    l.sync_bytes = l.nk > 1 ? kTicketBytes + sizeof(int) * items : 0;
-    size_t off = 256;
-    l.off_fsync = off;
-    off = up256(off + l.sync_bytes);
-    l.off_bsync = off;
-    off = up256(off + l.sync_bytes);
-    l.off_agg = off;
-    off = up256(off + (l.nk > 1 ? sizeof(float2) * items * tile : 0));
-    l.off_ckpt = off;
-    off = up256(off + sizeof(float) * items * tile);
-    l.off_adj = off;
-    off = up256(off + (l.nk > 1 ? sizeof(float) * items * tile : 0));
-    l.total = off;
+    l.nkf = cdiv(dm->seqlen, vscan_tokens());
+    l.nkb = cdiv(dm->seqlen, vscan_tokens_bwd());
+    l.off_ckpt = 256;
+    l.total = up256(l.off_ckpt + sizeof(float) * 2 * (size_t)(l.units * l.nkf) * tile);
     return l;
+}
+
+// Blocks per unit of the vector-state scan.
+int vscan_cluster(int64_t units, int64_t nk, int slots) {
+    if (g_vcluster > 0) return g_vcluster;
+    int cs = 1;
+    while (cs < 8 && cs < nk && units * cs < 4LL * slots) cs *= 2;
+    if (cs == 8 && nk > 8 && units * 16 <= slots) cs = 16;
+    return cs;
 }
 
 inline naju_status cuda_status(cudaError_t e) { return e == cudaSuccess ? NAJU_OK : NAJU_ERR_CUDA; }
@@ -312,7 +309,7 @@ naju_status check_dims(const naju_dims* dm) {
 namespace {
 
 // Dims of the vector-state scan: the sequence checks with d_state 1, and a
-// work-item count that fits the ticket.
+// unit count whose clusters fit one launch.
 naju_status check_vdims(const naju_dims* dm) {
     if (!dm) return NAJU_ERR_INVALID_ARG;
     naju_dims m = *dm;
@@ -320,18 +317,15 @@ naju_status check_vdims(const naju_dims* dm) {
     else return NAJU_ERR_UNSUPPORTED;
     const naju_status st = check_dims(&m);
     if (st != NAJU_OK) return st;
-    const int64_t items = dm->batch * cdiv(dm->d_inner, vscan_tile(dm->dtype)) *
-                          cdiv(dm->seqlen, vscan_tokens());
-    return items < (1LL << 31) - 1 ? NAJU_OK : NAJU_ERR_INVALID_ARG;
+    const int64_t units = dm->batch * cdiv(dm->d_inner, vscan_tile(dm->dtype));
+    return units < (1LL << 26) ? NAJU_OK : NAJU_ERR_INVALID_ARG;
 }
 
 void vscan_params(VscanParams& p, const naju_dims* dims, const VLayout& l, char* ws) {
     p.status = reinterpret_cast<int*>(ws);
-    p.agg = reinterpret_cast<float2*>(ws + l.off_agg);
     p.ckpt = reinterpret_cast<float*>(ws + l.off_ckpt);
-    p.adj = reinterpret_cast<float*>(ws + l.off_adj);
     p.L = dims->seqlen; p.d = dims->d_inner;
-    p.units = l.units; p.nk = l.nk; p.ntiles = (int)l.ntiles;
+    p.units = l.units; p.nck = 2 * l.nkf; p.ntiles = (int)l.ntiles;
     p.wait_limit = g_wait_limit;
     p.fault_skip_publish = g_skip_publish;
 }
@@ -534,15 +528,11 @@ naju_status naju_vscan_fwd(const naju_dims* dims, const void* h, const void* a, 
     NAJU_REQUIRE(workspace_bytes >= l.total);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
-    // status, ticket and flags in one go (one item per unit needs none of
-    // them: the kernel clears the status word itself)
-    if (l.nk > 1 && cudaMemsetAsync(ws, 0, l.off_fsync + l.sync_bytes, s) != cudaSuccess)
-        return NAJU_ERR_CUDA;
     VscanParams p{};
     vscan_params(p, dims, l, ws);
     p.h = h; p.a = a; p.b = b; p.z = z; p.x0 = x0; p.y = y; p.x_final = x_final;
-    p.ticket = reinterpret_cast<int*>(ws + l.off_fsync);
-    p.flags = reinterpret_cast<int*>(ws + l.off_fsync + kTicketBytes);
+    p.nk = l.nkf;
+    p.cluster = vscan_cluster(l.units, l.nkf, 3 * sm_count());
     return cuda_status(launch_vscan_fwd(p, dims->dtype, dims->out_dtype, s));
 }
 
@@ -560,14 +550,12 @@ naju_status naju_vscan_bwd(const naju_dims* dims, const void* h, const void* a, 
     NAJU_REQUIRE(workspace_bytes >= l.total);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
-    if (l.nk > 1 && cudaMemsetAsync(ws + l.off_bsync, 0, l.sync_bytes, s) != cudaSuccess)
-        return NAJU_ERR_CUDA;
     VscanParams p{};
     vscan_params(p, dims, l, ws);
     p.h = h; p.a = a; p.b = b; p.z = z; p.dy = dy; p.dx_final = dx_final;
     p.dh = dh; p.da = da; p.db = db; p.dz = dz; p.dx0 = dx0;
-    p.ticket = reinterpret_cast<int*>(ws + l.off_bsync);
-    p.flags = reinterpret_cast<int*>(ws + l.off_bsync + kTicketBytes);
+    p.nk = l.nkb;
+    p.cluster = vscan_cluster(l.units, l.nkb, 2 * sm_count());
     return cuda_status(launch_vscan_bwd(p, dims->dtype, dims->out_dtype, s));
 }
 
@@ -623,6 +611,9 @@ int32_t naju_testing_bwd_pieces(const void* dims) {
     const naju_dims* dm = static_cast<const naju_dims*>(dims);
     if (check_dims(dm) != NAJU_OK) return 0;
     return layout(dm).npieces;
+}
+void naju_testing_set_vscan_cluster(int32_t blocks) {
+    g_vcluster = blocks >= 1 && blocks <= 16 && (blocks & (blocks - 1)) == 0 ? blocks : 0;
 }
 void naju_testing_set_sm_count(int32_t sms) { g_sm_override = sms > 0 ? sms : 0; }
 int32_t naju_testing_sm_count(void) { return sm_count(); }

@@ -1,5 +1,6 @@
 // Internal launch interface between the C ABI layer and the kernels.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -151,19 +152,20 @@ struct VscanParams {
     void* dz;
     float* dx0;             // may be null
     int* status;
-    int* ticket;            // cleared before the launch, followed by the flags
-    int* flags;             // [units][nk]
-    float2* agg;            // [units][nk][tile]: an item's (P, X), backward (P, R)
-    float* ckpt;            // [units][nk][tile]: state entering each item
-    float* adj;             // [units][nk][tile]: adjoint leaving each item (backward)
+    float* ckpt;            // [units][nck][tile]: state at every backward item's start
     int64_t L, d;
-    int64_t units, nk;      // batch * channel tiles; items per unit
+    int64_t units, nk;      // batch * channel tiles; this direction's items per unit
+    int64_t nck;            // checkpoints per unit (two per forward item)
     int ntiles;
+    int cluster;            // blocks that share a unit
     long long wait_limit;
     int fault_skip_publish;
 };
 int vscan_tile(int dtype);  // channels per item
-int vscan_tokens();         // tokens per item
+int vscan_tokens();         // tokens per forward item
+int vscan_tokens_bwd();     // tokens per backward item and checkpoint
+bool vscan_map(CUtensorMap* map, const void* base, int64_t Bt, int64_t L, int64_t d, int dtype,
+               int rows);
 cudaError_t launch_vscan_fwd(const VscanParams& p, int dtype, int out_dtype, cudaStream_t st);
 cudaError_t launch_vscan_bwd(const VscanParams& p, int dtype, int out_dtype, cudaStream_t st);
 cudaError_t launch_vscan_step(int64_t n, const void* h, const void* a, const void* b,

@@ -4,167 +4,265 @@
 
 namespace naju {
 
-template <typename Tin, typename Tout, bool HASB, bool HASZ, bool VEC>
-__global__ void __launch_bounds__(256) vscan_fwd_kernel(VscanParams p) {
-    constexpr int CP = VRow<Tin>::CP, W = 32 * CP;
-    __shared__ float2 sagg[kVWarps][W];
-    __shared__ float sE[W];
-    __shared__ int s_item;
+struct VscanMaps {
+    CUtensorMap h, a, b, z;
+};
+
+// TMA: the item's rows come as one box of kVTokF rows x 128 bytes per tensor
+// (rows past the sequence and channels past the width read as zero);
+// otherwise every thread loads its own values.
+template <typename Tin, typename Tout, bool HASB, bool HASZ, bool TMA, bool VEC>
+__global__ void __launch_bounds__(kVThreads, 3)
+vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ VscanMaps maps) {
+    constexpr int CP = VRow<Tin>::CP, W = 32 * CP, RUN = kVRunF;
+    constexpr int kBox = kVTokF * 128;                // bytes of one tensor's box
+    constexpr int kNT = 2 + (HASB ? 1 : 0) + (HASZ ? 1 : 0);
+    typedef Vf<CP> V;
+    extern __shared__ __align__(128) unsigned char stage[];  // h, a, [b], [z]
+    __shared__ float2 sagg[2][kVWarps][W];  // (P, X) of each warp's tokens, by round parity
+    __shared__ float sE[2][W];              // the item's entering state
+    __shared__ VExchange<CP> ex;
+    __shared__ __align__(8) uint64_t full;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int64_t item = blockIdx.x;
-    if (p.nk > 1) {
-        if (tid == 0) s_item = atomicAdd(p.ticket, 1);
+    const uint32_t cs = p.cluster, rank = cluster_rank();
+    const unsigned u = blockIdx.x / cs;
+    const int64_t bb = u / p.ntiles;
+    const int c0 = (int)(u % p.ntiles) * W;
+    const int nk = (int)p.nk, rounds = (nk + (int)cs - 1) / (int)cs;
+
+    const auto fetch = [&](int k) {
+        const int x = (int)(u % p.ntiles) * 64, t = k * kVTokF;
+        tma::expect_tx(&full, kNT * kBox);
+        tma::load_3d(stage, &maps.h, x, t, (int)bb, &full);
+        tma::load_3d(stage + kBox, &maps.a, x, t, (int)bb, &full);
+        if (HASB) tma::load_3d(stage + 2 * kBox, &maps.b, x, t, (int)bb, &full);
+        if (HASZ) tma::load_3d(stage + (kNT - 1) * kBox, &maps.z, x, t, (int)bb, &full);
+    };
+    if (tid == 32 * kVWarps) {
+        ex.init();
+        if (TMA) {
+            mbar_init(&full, 1);
+            fence_proxy_async();
+            if ((int)rank < nk) fetch(rank);
+        }
+        if (blockIdx.x == 0) *p.status = 0;
+    }
+    __syncwarp();
+    if (cs > 1)
+        cluster_sync();  // every block's mbarriers exist before anything is sent to them
+    else
         __syncthreads();
-        item = s_item;
-    } else if (item == 0 && tid == 0) {
-        *p.status = 0;
-    }
-    const int64_t k = item / p.units, u = item % p.units;
-    const int64_t bb = u / p.ntiles, c0 = (u % p.ntiles) * W;
-    const int64_t t0 = k * kVTok + warp * kVRun;
-    const int64_t base = (bb * p.L + t0) * p.d;
-    const int n = (int)max64(0, min64(kVRun, p.L - t0));
 
-    uint32_t rh[kVRun], ra[kVRun], rb[kVRun], rz[kVRun];
-#pragma unroll
-    for (int q = 0; q < kVRun; ++q) {
-        const int64_t o = base + q * p.d;
-        if (q < n) {
-            ra[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.a) + o, c0, lane, p.d);
-            rh[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.h) + o, c0, lane, p.d);
-            if (HASB) rb[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.b) + o, c0, lane, p.d);
-            if (HASZ) rz[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.z) + o, c0, lane, p.d);
-        }
-    }
-    // gates; this warp's (P, X) from a zero state
-    float f[kVRun][CP], v[kVRun][CP], P[CP], X[CP];
-#pragma unroll
-    for (int j = 0; j < CP; ++j) P[j] = 1.f, X[j] = 0.f;
-#pragma unroll
-    for (int q = 0; q < kVRun; ++q) {
-        if (q < n) {
-            float a[CP], h[CP], b[CP];
-            VRow<Tin>::unpack(ra[q], a);
-            VRow<Tin>::unpack(rh[q], h);
-            if (HASB) VRow<Tin>::unpack(rb[q], b);
-#pragma unroll
-            for (int j = 0; j < CP; ++j) {
-                float fc;
-                gate2(a[j], f[q][j], fc);
-                v[q][j] = (HASB ? sigm(b[j]) : fc) * h[j];
-                P[j] *= f[q][j];
-                X[j] = fmaf(f[q][j], X[j], v[q][j]);
-            }
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < CP; ++j) sagg[warp][vchan<CP, VEC>(lane, j)] = make_float2(P[j], X[j]);
-    __syncthreads();
-
-    // warp 0: the item's entering state, and the one that leaves it
-    if (warp == 0) {
-        float PC[CP], XC[CP], E[CP];
-        int64_t ch[CP];
+    if (warp == kVWarps) {  // ------------------------------------- scout
+        float E[CP];
+        const int64_t row = bb * p.d + c0;
+        const int left = (int)min64(W, p.d - c0);
 #pragma unroll
         for (int j = 0; j < CP; ++j) {
-            ch[j] = vchan<CP, VEC>(lane, j);
-            PC[j] = 1.f, XC[j] = 0.f;
-#pragma unroll
-            for (int w = 0; w < kVWarps; ++w) {
-                const float2 g = sagg[w][ch[j]];
-                PC[j] *= g.x;
-                XC[j] = fmaf(g.x, XC[j], g.y);
-            }
+            const int ch = vchan<CP, VEC>(lane, j);
+            E[j] = p.x0 && ch < left ? p.x0[row + ch] : 0.f;
         }
-        int* flag = p.flags + u * p.nk + k;
-        float* ck = p.ckpt + u * p.nk * W;
-        const bool last = k + 1 == p.nk;
-        if (k == 0) {
+        bool alive = true;
+        for (int i = 0; i < rounds; ++i) {
+            const int par = i & 1, k = i * (int)cs + (int)rank;
+            named_bar(1, kVThreads);  // the warps' (P, X) are there, the tiles are read
+            if (TMA && lane == 0 && k + (int)cs < nk) fetch(k + cs);
+            float PC[CP], XC[CP], mine[CP];
 #pragma unroll
             for (int j = 0; j < CP; ++j) {
-                E[j] = p.x0 && c0 + ch[j] < p.d ? p.x0[bb * p.d + c0 + ch[j]] : 0.f;
-                ck[ch[j]] = E[j];
-            }
-        } else {
-            float2* ag = p.agg + u * p.nk * W;
-            if (!last) {
+                PC[j] = 1.f, XC[j] = 0.f;
 #pragma unroll
-                for (int j = 0; j < CP; ++j) __stcg(ag + k * W + ch[j], make_float2(PC[j], XC[j]));
-                vpublish(flag, kVAgg, lane);
-            }
-            const int dist = vlook(flag - 1, -1, k, lane, p.status, p.wait_limit);
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < CP; ++j) {
-                E[j] = dist ? __ldcg(ck + (k - dist + 1) * W + ch[j]) : 0.f;
-                for (int i = dist - 1; i >= 1; --i) {
-                    const float2 g = __ldcg(ag + (k - i) * W + ch[j]);
-                    E[j] = fmaf(g.x, E[j], g.y);
+                for (int w = 0; w < kVWarps; ++w) {
+                    const float2 g = sagg[par][w][lane * CP + j];
+                    PC[j] *= g.x;
+                    XC[j] = fmaf(g.x, XC[j], g.y);
                 }
             }
-        }
+            if (cs > 1) {
+                ex.round(i, rank, cs, lane, PC, XC, E, mine, alive,
+                         p.fault_skip_publish && i == 0 && rank == 0, p.status, p.wait_limit);
+            } else {
 #pragma unroll
-        for (int j = 0; j < CP; ++j) {
-            sE[ch[j]] = E[j];
-            const float out = fmaf(PC[j], E[j], XC[j]);
-            if (!last)
-                __stcg(ck + (k + 1) * W + ch[j], out);
-            else if (p.x_final && c0 + ch[j] < p.d)
-                p.x_final[bb * p.d + c0 + ch[j]] = out;
-        }
-        if (!last && !(p.fault_skip_publish && k == 0)) vpublish(flag, kVIncl, lane);
-    }
-    __syncthreads();
-
-    // every warp: its entering state, then its tokens
-    float x[CP];
+                for (int j = 0; j < CP; ++j) {
+                    mine[j] = E[j];
+                    E[j] = fmaf(PC[j], E[j], XC[j]);
+                }
+            }
 #pragma unroll
-    for (int j = 0; j < CP; ++j) {
-        const int ch = vchan<CP, VEC>(lane, j);
-        x[j] = sE[ch];
-        for (int w = 0; w < warp; ++w) {
-            const float2 g = sagg[w][ch];
-            x[j] = fmaf(g.x, x[j], g.y);
-        }
-    }
-    Tout* y = static_cast<Tout*>(p.y) + base;
+            for (int j = 0; j < CP; ++j) sE[par][lane * CP + j] = mine[j];
+            named_arrive(2, kVThreads);
+            if (k < nk) {
+                float* ck = p.ckpt + ((int64_t)u * p.nck + 2 * k) * W;
 #pragma unroll
-    for (int q = 0; q < kVRun; ++q) {
-        if (q < n) {
-            float o[CP], z[CP];
-            if (HASZ) VRow<Tin>::unpack(rz[q], z);
+                for (int j = 0; j < CP; ++j) ck[vchan<CP, VEC>(lane, j)] = mine[j];
+            }
+        }
+        if (rank == 0 && p.x_final) {
 #pragma unroll
             for (int j = 0; j < CP; ++j) {
-                x[j] = fmaf(f[q][j], x[j], v[q][j]);
-                o[j] = HASZ ? x[j] * (z[j] * sigm(z[j])) : x[j];
+                const int ch = vchan<CP, VEC>(lane, j);
+                if (ch < left) p.x_final[row + ch] = E[j];
             }
-            vstore<Tout, CP, VEC>(y + q * p.d, c0, lane, p.d, o);
         }
+    } else {  // ------------------------------------------- compute warps
+        const int cl = c0 + vchan<CP, VEC>(lane, 0);
+        const int left = (int)p.d - cl;
+        const uint32_t stride = (uint32_t)p.d * sizeof(Tout);
+        const uint32_t off0 = ((uint32_t)(warp * RUN) * (uint32_t)p.d + cl) * sizeof(Tout);
+        for (int i = 0; i < rounds; ++i) {
+            const int par = i & 1, k = i * (int)cs + (int)rank;
+            const int64_t tile = (bb * p.L + (int64_t)k * kVTokF) * p.d;  // uniform
+            // this warp's tokens (<= 0: none)
+            const int n = k < nk ? (int)min64(RUN, p.L - k * kVTokF - warp * RUN) : 0;
+            V f[RUN], v[RUN], P = vset<CP>(1.f), X = vset<CP>(0.f);
+            uint32_t rz[RUN];
+            if (n > 0) {
+                uint32_t rh[RUN], ra[RUN], rb[RUN];
+                if (TMA) {
+                    if (!mbar_wait(&full, par, kTmaPolls))
+                        atomicOr(p.status, 1 << NAJU_ERR_TIMEOUT);
+                    const unsigned char* at = stage + warp * RUN * 128 + lane * 4;
+                    const auto get = [&](int which, int q) {
+                        return *reinterpret_cast<const uint32_t*>(at + which * kBox + q * 128);
+                    };
+#pragma unroll
+                    for (int q = 0; q < RUN; ++q) {
+                        rh[q] = get(0, q);
+                        ra[q] = get(1, q);
+                        if (HASB) rb[q] = get(2, q);
+                        if (HASZ) rz[q] = get(kNT - 1, q);
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < RUN; ++q) {
+                        rh[q] = ra[q] = rb[q] = rz[q] = 0;
+                        if (q < n) {
+                            const int64_t o = tile + (int64_t)(warp * RUN + q) * p.d;
+                            ra[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.a) + o, c0, lane, p.d);
+                            rh[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.h) + o, c0, lane, p.d);
+                            if (HASB)
+                                rb[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.b) + o, c0, lane,
+                                                        p.d);
+                            if (HASZ)
+                                rz[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.z) + o, c0, lane,
+                                                        p.d);
+                        }
+                    }
+                }
+                // gates; this warp's (P, X) from a zero state
+#pragma unroll
+                for (int q = 0; q < RUN; ++q) {
+                    V r, s, fc;
+                    gate_rs<Tin>(ra[q], r, s);
+                    gate_sel<Tin>(ra[q], r, s, f[q], fc);
+                    v[q] = (HASB ? vsigm<CP>(VRow<Tin>::unpack(rb[q])) : fc) *
+                           VRow<Tin>::unpack(rh[q]);
+                }
+                if (n < RUN) {  // past the sequence: the identity
+#pragma unroll
+                    for (int q = 0; q < RUN; ++q)
+                        if (q >= n) f[q] = vset<CP>(1.f), v[q] = vset<CP>(0.f);
+                }
+#pragma unroll
+                for (int q = 0; q < RUN; ++q) {
+                    P = P * f[q];
+                    X = vfma(f[q], X, v[q]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < CP; ++j) sagg[par][warp][lane * CP + j] = make_float2(P[j], X[j]);
+            named_bar(1, kVThreads);
+            named_bar(2, kVThreads);
+            if (n <= 0) continue;
+            // this warp's entering state, then its tokens
+            V x;
+#pragma unroll
+            for (int j = 0; j < CP; ++j) x[j] = sE[par][lane * CP + j];
+            for (int w = 0; w < warp; ++w) {
+#pragma unroll
+                for (int j = 0; j < CP; ++j) {
+                    const float2 g = sagg[par][w][lane * CP + j];
+                    x[j] = fmaf(g.x, x[j], g.y);
+                }
+            }
+            if (warp == kVWarps / 2) {  // the checkpoint inside the item
+                float* ck = p.ckpt + ((int64_t)u * p.nck + 2 * k + 1) * W;
+#pragma unroll
+                for (int j = 0; j < CP; ++j) ck[vchan<CP, VEC>(lane, j)] = x[j];
+            }
+            char* y = reinterpret_cast<char*>(static_cast<Tout*>(p.y) + tile);
+            const auto token = [&](int q) {
+                x = vfma(f[q], x, v[q]);
+                V o = x;
+                if (HASZ) {
+                    const V z = VRow<Tin>::unpack(rz[q]);
+                    o = x * (z * vsigm<CP>(z));
+                }
+                vstore<Tout, CP, VEC>(reinterpret_cast<Tout*>(y + (off0 + q * stride)), left, o);
+            };
+            if (n == RUN) {
+#pragma unroll
+                for (int q = 0; q < RUN; ++q) token(q);
+            } else {
+#pragma unroll
+                for (int q = 0; q < RUN; ++q)
+                    if (q < n) token(q);
+            }
+        }
+    }
+    // no block leaves while another may still send to it
+    if (cs > 1) {
+        __syncwarp();
+        cluster_sync();
     }
 }
 
-template <typename Tin, typename Tout, bool VEC>
-static cudaError_t fwd_t(const VscanParams& p, cudaStream_t st) {
-    const unsigned grid = (unsigned)(p.units * p.nk);
+template <typename Tin, typename Tout, bool HASB, bool HASZ, bool TMA, bool VEC>
+static cudaError_t fwd_k(const VscanParams& p, const VscanMaps& maps, cudaStream_t st) {
+    const int smem = TMA ? (2 + HASB + HASZ) * kVTokF * 128 : 0;
+    return vscan_launch(vscan_fwd_kernel<Tin, Tout, HASB, HASZ, TMA, VEC>, p, maps, smem, st);
+}
+
+template <typename Tin, typename Tout, bool TMA, bool VEC>
+static cudaError_t fwd_t(const VscanParams& p, const VscanMaps& m, cudaStream_t st) {
     if (p.b)
-        p.z ? vscan_fwd_kernel<Tin, Tout, true, true, VEC><<<grid, 256, 0, st>>>(p)
-            : vscan_fwd_kernel<Tin, Tout, true, false, VEC><<<grid, 256, 0, st>>>(p);
-    else
-        p.z ? vscan_fwd_kernel<Tin, Tout, false, true, VEC><<<grid, 256, 0, st>>>(p)
-            : vscan_fwd_kernel<Tin, Tout, false, false, VEC><<<grid, 256, 0, st>>>(p);
-    return cudaGetLastError();
+        return p.z ? fwd_k<Tin, Tout, true, true, TMA, VEC>(p, m, st)
+                   : fwd_k<Tin, Tout, true, false, TMA, VEC>(p, m, st);
+    return p.z ? fwd_k<Tin, Tout, false, true, TMA, VEC>(p, m, st)
+               : fwd_k<Tin, Tout, false, false, TMA, VEC>(p, m, st);
+}
+
+// Rows as 2-byte elements (TMA moves bits; an fp32 value is two of them).
+bool vscan_map(CUtensorMap* map, const void* base, int64_t Bt, int64_t L, int64_t d, int dtype,
+               int rows) {
+    return tma_encode_bf16_3d(map, base, Bt, L, dtype == NAJU_F32 ? 2 * d : d, rows, 64);
 }
 
 cudaError_t launch_vscan_fwd(const VscanParams& p, int dtype, int out_dtype, cudaStream_t st) {
     typedef __nv_bfloat16 bf;
-    if (dtype == NAJU_F32) return fwd_t<float, float, true>(p, st);
-    const bool vec = p.d % 2 == 0;
-    if (out_dtype == NAJU_BF16) return vec ? fwd_t<bf, bf, true>(p, st) : fwd_t<bf, bf, false>(p, st);
-    return vec ? fwd_t<bf, float, true>(p, st) : fwd_t<bf, float, false>(p, st);
+    const int64_t Bt = p.units / p.ntiles;
+    VscanMaps m{};
+    if (p.d * (dtype == NAJU_F32 ? 4 : 2) % 16 == 0) {
+        const auto enc = [&](CUtensorMap* map, const void* base) {
+            return !base || vscan_map(map, base, Bt, p.L, p.d, dtype, kVTokF);
+        };
+        if (!(enc(&m.h, p.h) && enc(&m.a, p.a) && enc(&m.b, p.b) && enc(&m.z, p.z)))
+            return cudaErrorInvalidValue;
+        if (dtype == NAJU_F32) return fwd_t<float, float, true, true>(p, m, st);
+        return out_dtype == NAJU_BF16 ? fwd_t<bf, bf, true, true>(p, m, st)
+                                      : fwd_t<bf, float, true, true>(p, m, st);
+    }
+    if (dtype == NAJU_F32) return fwd_t<float, float, false, true>(p, m, st);
+    if (p.d % 2 == 0)
+        return out_dtype == NAJU_BF16 ? fwd_t<bf, bf, false, true>(p, m, st)
+                                      : fwd_t<bf, float, false, true>(p, m, st);
+    return out_dtype == NAJU_BF16 ? fwd_t<bf, bf, false, false>(p, m, st)
+                                  : fwd_t<bf, float, false, false>(p, m, st);
 }
 
 int vscan_tile(int dtype) { return dtype == NAJU_F32 ? 32 : 64; }
-int vscan_tokens() { return kVTok; }
+int vscan_tokens() { return kVTokF; }
+int vscan_tokens_bwd() { return kVTokB; }
 
 // ------------------------------------------------------------ decode step
 // Elementwise over batch * d_inner: 8 consecutive values per thread (16-byte
@@ -198,10 +296,12 @@ vscan_step_kernel(int64_t n, const T* __restrict__ h, const T* __restrict__ a,
     float o[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        float f, fc;
-        gate2(av[k], f, fc);
-        x[k] = fmaf(f, x[k], (b ? sigm(bv[k]) : fc) * hv[k]);
-        o[k] = z ? x[k] * (zv[k] * sigm(zv[k])) : x[k];
+        const uint32_t bits = __float_as_uint(av[k]);
+        Vf<1> r, s, f, fc;
+        gate_rs<float>(bits, r, s);
+        gate_sel<float>(bits, r, s, f, fc);
+        x[k] = fmaf(f.x, x[k], (b ? sigmoidx_(bv[k]) : fc.x) * hv[k]);
+        o[k] = z ? x[k] * (zv[k] * sigmoidx_(zv[k])) : x[k];
     }
     if (m == 8) {
         store8(state + e0, x);

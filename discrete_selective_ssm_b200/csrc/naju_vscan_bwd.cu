@@ -3,240 +3,312 @@
 // With dx_t = dy_t SiLU(z_t) the adjoint is g_t = dx_t + r_{t+1}, where
 // r_t = f_t g_t is what a token hands to the one before it (r_L = dx_final,
 // r_0 = dx0).  A run of tokens acts on r as r -> P r + R with the forward's
-// own P, so the runs compose like the forward's, in the other direction.  The
-// gradients also need x_{t-1}: each item recomputes its states from the
-// forward's checkpoint of its first token (one fp32 value per kVTok tokens)
-// instead of reading stored states.
+// own P, so the runs compose like the forward's, in the other direction:
+//   dh = g i,  db = g h i (1 - i),  da = g f (1 - f) x_{t-1}  (coupled:
+//   x_{t-1} - h in its place),  dz = dy SiLU'(z) x.
+// The states are recomputed from the forward's checkpoints (one fp32 value per
+// 32 tokens and channel), which costs one multiply-add a token and saves
+// reading them.
 #include "naju_kernels.h"
 #include "naju_vscan.cuh"
 
 namespace naju {
 
-template <typename Tin, typename Tout, bool HASB, bool HASZ, bool VEC>
-__global__ void __launch_bounds__(256) vscan_bwd_kernel(VscanParams p) {
-    constexpr int CP = VRow<Tin>::CP, W = 32 * CP;
-    __shared__ float2 sagg[kVWarps][W];  // (P, X) of each warp's tokens
-    __shared__ float srev[kVWarps][W];   // R of each warp's tokens
-    __shared__ float sE[W], sA[W];
-    __shared__ int s_item;
+struct VscanBwdMaps {
+    CUtensorMap h, a, b, z, dy;
+};
+
+template <typename Tin, typename Tout, bool HASB, bool HASZ, bool TMA, bool VEC>
+__global__ void __launch_bounds__(kVThreads, 2)
+vscan_bwd_kernel(const __grid_constant__ VscanParams p,
+                 const __grid_constant__ VscanBwdMaps maps) {
+    constexpr int CP = VRow<Tin>::CP, W = 32 * CP, RUN = kVRunB;
+    constexpr int kBox = kVTokB * 128;
+    constexpr int kNT = 3 + (HASB ? 1 : 0) + (HASZ ? 1 : 0);
+    typedef Vf<CP> V;
+    extern __shared__ __align__(128) unsigned char stage[];  // h, a, dy, [b], [z]
+    __shared__ float4 sagg[2][kVWarps][W];  // (P, X, R) of each warp's tokens, by round parity
+    __shared__ float sE[2][W], sA[2][W];    // the item's entering state and adjoint
+    __shared__ VExchange<CP> ex;
+    __shared__ __align__(8) uint64_t full;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int64_t item = blockIdx.x;
-    if (p.nk > 1) {
-        if (tid == 0) s_item = atomicAdd(p.ticket, 1);
+    const uint32_t cs = p.cluster, rank = cluster_rank();
+    const unsigned u = blockIdx.x / cs;
+    const int64_t bb = u / p.ntiles;
+    const int c0 = (int)(u % p.ntiles) * W;
+    // items in the order in which they are walked: o = 0 is the last one
+    const int nk = (int)p.nk, rounds = (nk + (int)cs - 1) / (int)cs;
+
+    const auto fetch = [&](int o) {
+        const int x = (int)(u % p.ntiles) * 64, t = (nk - 1 - o) * kVTokB;
+        tma::expect_tx(&full, kNT * kBox);
+        tma::load_3d(stage, &maps.h, x, t, (int)bb, &full);
+        tma::load_3d(stage + kBox, &maps.a, x, t, (int)bb, &full);
+        tma::load_3d(stage + 2 * kBox, &maps.dy, x, t, (int)bb, &full);
+        if (HASB) tma::load_3d(stage + 3 * kBox, &maps.b, x, t, (int)bb, &full);
+        if (HASZ) tma::load_3d(stage + (kNT - 1) * kBox, &maps.z, x, t, (int)bb, &full);
+    };
+    if (tid == 32 * kVWarps) {
+        ex.init();
+        if (TMA) {
+            mbar_init(&full, 1);
+            fence_proxy_async();
+            if ((int)rank < nk) fetch(rank);
+        }
+    }
+    __syncwarp();
+    if (cs > 1)
+        cluster_sync();  // every block's mbarriers exist before anything is sent to them
+    else
         __syncthreads();
-        item = s_item;
-    }
-    const int64_t k = p.nk - 1 - item / p.units, u = item % p.units;
-    const int64_t bb = u / p.ntiles, c0 = (u % p.ntiles) * W;
-    const int64_t t0 = k * kVTok + warp * kVRun;
-    const int64_t base = (bb * p.L + t0) * p.d;
-    const int n = (int)max64(0, min64(kVRun, p.L - t0));
 
-    uint32_t rh[kVRun], ra[kVRun], rb[kVRun], rz[kVRun], rd[kVRun];
-#pragma unroll
-    for (int q = 0; q < kVRun; ++q) {
-        const int64_t o = base + q * p.d;
-        if (q < n) {
-            ra[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.a) + o, c0, lane, p.d);
-            rh[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.h) + o, c0, lane, p.d);
-            rd[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.dy) + o, c0, lane, p.d);
-            if (HASB) rb[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.b) + o, c0, lane, p.d);
-            if (HASZ) rz[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.z) + o, c0, lane, p.d);
-        }
-    }
-    float E0[CP];  // warp 0: the item's entering state
-    if (warp == 0) {
-#pragma unroll
-        for (int j = 0; j < CP; ++j)
-            E0[j] = p.ckpt[(u * p.nk + k) * W + vchan<CP, VEC>(lane, j)];
-    }
-    // Kept per token: both gates packed, sigmoid(z).
-    float ga[kVRun][CP], gb[kVRun][CP], sz[kVRun][CP], P[CP], X[CP], R[CP];
-#pragma unroll
-    for (int j = 0; j < CP; ++j) P[j] = 1.f, X[j] = 0.f, R[j] = 0.f;
-#pragma unroll
-    for (int q = 0; q < kVRun; ++q) {
-        if (q < n) {
-            float a[CP], h[CP], b[CP], z[CP];
-            VRow<Tin>::unpack(ra[q], a);
-            VRow<Tin>::unpack(rh[q], h);
-            if (HASB) VRow<Tin>::unpack(rb[q], b);
-            if (HASZ) VRow<Tin>::unpack(rz[q], z);
-#pragma unroll
-            for (int j = 0; j < CP; ++j) {
-                float f, fc, i, ic;
-                ga[q][j] = gate_pack(a[j]);
-                gate_of(ga[q][j], f, fc);
-                if (HASB) {
-                    gb[q][j] = gate_pack(b[j]);
-                    gate_of(gb[q][j], i, ic);
-                } else {
-                    i = fc;
-                }
-                if (HASZ) sz[q][j] = sigm(z[j]);
-                P[j] *= f;
-                X[j] = fmaf(f, X[j], i * h[j]);
-            }
-        }
-    }
-#pragma unroll
-    for (int q = kVRun - 1; q >= 0; --q) {
-        if (q < n) {
-            float dy[CP], z[CP];
-            VRow<Tin>::unpack(rd[q], dy);
-            if (HASZ) VRow<Tin>::unpack(rz[q], z);
-#pragma unroll
-            for (int j = 0; j < CP; ++j) {
-                float f, fc;
-                gate_of(ga[q][j], f, fc);
-                const float dx = HASZ ? dy[j] * (z[j] * sz[q][j]) : dy[j];
-                R[j] = f * (dx + R[j]);
-            }
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < CP; ++j) {
-        const int ch = vchan<CP, VEC>(lane, j);
-        sagg[warp][ch] = make_float2(P[j], X[j]);
-        srev[warp][ch] = R[j];
-    }
-    __syncthreads();
-
-    if (warp == 0) {
-        float PC[CP], RC[CP], A[CP];
-        int64_t ch[CP];
-#pragma unroll
-        for (int j = 0; j < CP; ++j) {
-            ch[j] = vchan<CP, VEC>(lane, j);
-            PC[j] = 1.f, RC[j] = 0.f;
-#pragma unroll
-            for (int w = kVWarps - 1; w >= 0; --w) {
-                const float g = sagg[w][ch[j]].x;
-                PC[j] *= g;
-                RC[j] = fmaf(g, RC[j], srev[w][ch[j]]);
-            }
-        }
-        int* flag = p.flags + u * p.nk + k;
-        float* adj = p.adj + u * p.nk * W;  // r leaving item k, at k
-        if (k + 1 == p.nk) {
+    if (warp == kVWarps) {  // ------------------------------------- scout
+        float A[CP], E0[CP];
+        const int64_t row = bb * p.d + c0;
+        const int left = (int)min64(W, p.d - c0);
+        const auto state = [&](int o) {  // the checkpoint at the start of item o
 #pragma unroll
             for (int j = 0; j < CP; ++j)
-                A[j] = p.dx_final && c0 + ch[j] < p.d ? p.dx_final[bb * p.d + c0 + ch[j]] : 0.f;
-        } else {
-            float2* ag = p.agg + u * p.nk * W;
-            if (k > 0) {
-#pragma unroll
-                for (int j = 0; j < CP; ++j) __stcg(ag + k * W + ch[j], make_float2(PC[j], RC[j]));
-                vpublish(flag, kVAgg, lane);
-            }
-            const int dist = vlook(flag + 1, 1, p.nk - 1 - k, lane, p.status, p.wait_limit);
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < CP; ++j) {
-                A[j] = dist ? __ldcg(adj + (k + dist) * W + ch[j]) : 0.f;
-                for (int i = dist - 1; i >= 1; --i) {
-                    const float2 g = __ldcg(ag + (k + i) * W + ch[j]);
-                    A[j] = fmaf(g.x, A[j], g.y);
-                }
-            }
-        }
+                E0[j] = o < nk ? p.ckpt[((int64_t)u * p.nck + (nk - 1 - o)) * W +
+                                        vchan<CP, VEC>(lane, j)]
+                               : 0.f;
+        };
 #pragma unroll
         for (int j = 0; j < CP; ++j) {
-            sE[ch[j]] = E0[j];
-            sA[ch[j]] = A[j];
-            const float out = fmaf(PC[j], A[j], RC[j]);
-            if (k > 0)
-                __stcg(adj + k * W + ch[j], out);
-            else if (p.dx0 && c0 + ch[j] < p.d)
-                p.dx0[bb * p.d + c0 + ch[j]] = out;
+            const int ch = vchan<CP, VEC>(lane, j);
+            A[j] = p.dx_final && ch < left ? p.dx_final[row + ch] : 0.f;
         }
-        if (k > 0 && !(p.fault_skip_publish && k + 1 == p.nk)) vpublish(flag, kVIncl, lane);
-    }
-    __syncthreads();
-
-    float x[CP], r[CP], xs[kVRun + 1][CP];
+        state(rank);
+        bool alive = true;
+        for (int i = 0; i < rounds; ++i) {
+            const int par = i & 1, o = i * (int)cs + (int)rank;
 #pragma unroll
-    for (int j = 0; j < CP; ++j) {
-        const int ch = vchan<CP, VEC>(lane, j);
-        x[j] = sE[ch];
-        for (int w = 0; w < warp; ++w) {
-            const float2 g = sagg[w][ch];
-            x[j] = fmaf(g.x, x[j], g.y);
-        }
-        r[j] = sA[ch];
-        for (int w = kVWarps - 1; w > warp; --w) r[j] = fmaf(sagg[w][ch].x, r[j], srev[w][ch]);
-        xs[0][j] = x[j];
-    }
-#pragma unroll
-    for (int q = 0; q < kVRun; ++q) {
-        if (q < n) {
-            float h[CP];
-            VRow<Tin>::unpack(rh[q], h);
+            for (int j = 0; j < CP; ++j) sE[par][lane * CP + j] = E0[j];
+            state(o + (int)cs);
+            named_bar(1, kVThreads);  // the warps' sums are there, the tiles are read
+            if (TMA && lane == 0 && o + (int)cs < nk) fetch(o + cs);
+            float PC[CP], RC[CP], mine[CP];
 #pragma unroll
             for (int j = 0; j < CP; ++j) {
-                float f, fc, i, ic;
-                gate_of(ga[q][j], f, fc);
-                if (HASB) gate_of(gb[q][j], i, ic);
-                xs[q + 1][j] = fmaf(f, xs[q][j], (HASB ? i : fc) * h[j]);
+                PC[j] = 1.f, RC[j] = 0.f;
+#pragma unroll
+                for (int w = kVWarps - 1; w >= 0; --w) {
+                    const float4 g = sagg[par][w][lane * CP + j];
+                    PC[j] *= g.x;
+                    RC[j] = fmaf(g.x, RC[j], g.z);
+                }
+            }
+            if (cs > 1) {
+                ex.round(i, rank, cs, lane, PC, RC, A, mine, alive,
+                         p.fault_skip_publish && i == 0 && rank == 0, p.status, p.wait_limit);
+            } else {
+#pragma unroll
+                for (int j = 0; j < CP; ++j) {
+                    mine[j] = A[j];
+                    A[j] = fmaf(PC[j], A[j], RC[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < CP; ++j) sA[par][lane * CP + j] = mine[j];
+            named_arrive(2, kVThreads);
+        }
+        if (rank == 0 && p.dx0) {
+#pragma unroll
+            for (int j = 0; j < CP; ++j) {
+                const int ch = vchan<CP, VEC>(lane, j);
+                if (ch < left) p.dx0[row + ch] = A[j];
             }
         }
-    }
+    } else {  // ------------------------------------------- compute warps
+        const int cl = c0 + vchan<CP, VEC>(lane, 0);
+        const int left = (int)p.d - cl;
+        const uint32_t stride = (uint32_t)p.d * sizeof(Tout);
+        const uint32_t off0 = ((uint32_t)(warp * RUN) * (uint32_t)p.d + cl) * sizeof(Tout);
+        const V one = vset<CP>(1.f), minus = vset<CP>(-1.f);
+        for (int i = 0; i < rounds; ++i) {
+            const int par = i & 1, k = nk - 1 - (i * (int)cs + (int)rank);
+            const int64_t tile = (bb * p.L + (int64_t)k * kVTokB) * p.d;  // uniform
+            // this warp's tokens (<= 0: none)
+            const int n = k >= 0 ? (int)min64(RUN, p.L - k * kVTokB - warp * RUN) : 0;
+            // Kept per token: f, i, v = i h, dx, and the factors of g, g and x
+            // in da, db and dz: m = f (1 - f), w = h i (1 - i) (coupled: -m h),
+            // e = dy SiLU'(z).
+            V f[RUN], m[RUN], gi[RUN], v[RUN], w[RUN], dx[RUN], e[RUN];
+            V P = one, X = vset<CP>(0.f), R = vset<CP>(0.f);
+            if (n > 0) {
+                uint32_t rh[RUN], ra[RUN], rb[RUN], rz[RUN], rd[RUN];
+                if (TMA) {
+                    if (!mbar_wait(&full, par, kTmaPolls))
+                        atomicOr(p.status, 1 << NAJU_ERR_TIMEOUT);
+                    const unsigned char* at = stage + warp * RUN * 128 + lane * 4;
+                    const auto get = [&](int which, int q) {
+                        return *reinterpret_cast<const uint32_t*>(at + which * kBox + q * 128);
+                    };
 #pragma unroll
-    for (int q = kVRun - 1; q >= 0; --q) {
-        if (q < n) {
-            float dy[CP], h[CP], z[CP], oh[CP], oa[CP], ob[CP], oz[CP];
-            VRow<Tin>::unpack(rd[q], dy);
-            VRow<Tin>::unpack(rh[q], h);
-            if (HASZ) VRow<Tin>::unpack(rz[q], z);
-#pragma unroll
-            for (int j = 0; j < CP; ++j) {
-                float f, fc, i, ic;
-                gate_of(ga[q][j], f, fc);
-                float dx = dy[j];
-                if (HASZ) {
-                    const float s = sz[q][j], zs = z[j] * s;
-                    // SiLU'(z) = s + z s (1 - s)
-                    oz[j] = dy[j] * xs[q + 1][j] * fmaf(zs, 1.f - s, s);
-                    dx *= zs;
-                }
-                const float g = dx + r[j];
-                r[j] = f * g;
-                oa[j] = (r[j] * fc) * (HASB ? xs[q][j] : xs[q][j] - h[j]);
-                if (HASB) {
-                    gate_of(gb[q][j], i, ic);
-                    oh[j] = g * i;
-                    ob[j] = oh[j] * (h[j] * ic);
+                    for (int q = 0; q < RUN; ++q) {
+                        rh[q] = get(0, q);
+                        ra[q] = get(1, q);
+                        rd[q] = get(2, q);
+                        if (HASB) rb[q] = get(3, q);
+                        if (HASZ) rz[q] = get(kNT - 1, q);
+                    }
                 } else {
-                    oh[j] = g * fc;
+#pragma unroll
+                    for (int q = 0; q < RUN; ++q) {
+                        rh[q] = ra[q] = rb[q] = rz[q] = rd[q] = 0;
+                        if (q < n) {
+                            const int64_t o = tile + (int64_t)(warp * RUN + q) * p.d;
+                            ra[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.a) + o, c0, lane, p.d);
+                            rh[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.h) + o, c0, lane, p.d);
+                            rd[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.dy) + o, c0, lane,
+                                                    p.d);
+                            if (HASB)
+                                rb[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.b) + o, c0, lane,
+                                                        p.d);
+                            if (HASZ)
+                                rz[q] = vload<Tin, VEC>(static_cast<const Tin*>(p.z) + o, c0, lane,
+                                                        p.d);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < RUN; ++q) {
+                    const V h = VRow<Tin>::unpack(rh[q]), dy = VRow<Tin>::unpack(rd[q]);
+                    V r, s, fc;
+                    gate_rs<Tin>(ra[q], r, s);
+                    gate_sel<Tin>(ra[q], r, s, f[q], fc);
+                    m[q] = r * s;
+                    if (HASB) {
+                        gate_rs<Tin>(rb[q], r, s);
+                        V ic;
+                        gate_sel<Tin>(rb[q], r, s, gi[q], ic);
+                        w[q] = h * (r * s);
+                    } else {
+                        gi[q] = fc;
+                        w[q] = m[q] * h * minus;
+                    }
+                    v[q] = gi[q] * h;
+                    if (HASZ) {
+                        const V z = VRow<Tin>::unpack(rz[q]);
+                        const V sz = vsigm<CP>(z), zs = z * sz;
+                        e[q] = dy * vfma(zs, vfma(sz, minus, one), sz);  // s + z s (1 - s)
+                        dx[q] = dy * zs;
+                    } else {
+                        dx[q] = dy;
+                    }
+                }
+                if (n < RUN) {  // past the sequence: the identity
+#pragma unroll
+                    for (int q = 0; q < RUN; ++q)
+                        if (q >= n) f[q] = one, v[q] = dx[q] = vset<CP>(0.f);
+                }
+#pragma unroll
+                for (int q = 0; q < RUN; ++q) {
+                    P = P * f[q];
+                    X = vfma(f[q], X, v[q]);
+                    const int rq = RUN - 1 - q;
+                    R = f[rq] * (dx[rq] + R);
                 }
             }
-            const int64_t o = base + q * p.d;
-            vstore<Tout, CP, VEC>(static_cast<Tout*>(p.dh) + o, c0, lane, p.d, oh);
-            vstore<Tout, CP, VEC>(static_cast<Tout*>(p.da) + o, c0, lane, p.d, oa);
-            if (HASB) vstore<Tout, CP, VEC>(static_cast<Tout*>(p.db) + o, c0, lane, p.d, ob);
-            if (HASZ) vstore<Tout, CP, VEC>(static_cast<Tout*>(p.dz) + o, c0, lane, p.d, oz);
+#pragma unroll
+            for (int j = 0; j < CP; ++j)
+                sagg[par][warp][lane * CP + j] = make_float4(P[j], X[j], R[j], 0.f);
+            named_bar(1, kVThreads);
+            // the states need no exchange: they go before the second barrier
+            V xs[RUN + 1], r;
+            if (n > 0) {
+#pragma unroll
+                for (int j = 0; j < CP; ++j) xs[0][j] = sE[par][lane * CP + j];
+                for (int o = 0; o < warp; ++o) {
+#pragma unroll
+                    for (int j = 0; j < CP; ++j) {
+                        const float4 g = sagg[par][o][lane * CP + j];
+                        xs[0][j] = fmaf(g.x, xs[0][j], g.y);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < RUN; ++q) {
+                    xs[q + 1] = vfma(f[q], xs[q], v[q]);
+                    m[q] = HASB ? m[q] * xs[q] : vfma(m[q], xs[q], w[q]);  // da / g
+                    if (HASZ) e[q] = e[q] * xs[q + 1];                     // dz
+                }
+            }
+            named_bar(2, kVThreads);
+            if (n <= 0) continue;
+#pragma unroll
+            for (int j = 0; j < CP; ++j) r[j] = sA[par][lane * CP + j];
+            for (int o = kVWarps - 1; o > warp; --o) {
+#pragma unroll
+                for (int j = 0; j < CP; ++j) {
+                    const float4 g = sagg[par][o][lane * CP + j];
+                    r[j] = fmaf(g.x, r[j], g.z);
+                }
+            }
+            const auto at = [&](void* t, int q) {
+                return reinterpret_cast<Tout*>(
+                    reinterpret_cast<char*>(static_cast<Tout*>(t) + tile) + (off0 + q * stride));
+            };
+            const auto token = [&](int q) {
+                const V g = dx[q] + r;
+                r = f[q] * g;
+                vstore<Tout, CP, VEC>(at(p.dh, q), left, g * gi[q]);
+                vstore<Tout, CP, VEC>(at(p.da, q), left, g * m[q]);
+                if (HASB) vstore<Tout, CP, VEC>(at(p.db, q), left, g * w[q]);
+                if (HASZ) vstore<Tout, CP, VEC>(at(p.dz, q), left, e[q]);
+            };
+            if (n == RUN) {
+#pragma unroll
+                for (int q = RUN - 1; q >= 0; --q) token(q);
+            } else {
+#pragma unroll
+                for (int q = RUN - 1; q >= 0; --q)
+                    if (q < n) token(q);
+            }
         }
+    }
+    // no block leaves while another may still send to it
+    if (cs > 1) {
+        __syncwarp();
+        cluster_sync();
     }
 }
 
-template <typename Tin, typename Tout, bool VEC>
-static cudaError_t bwd_t(const VscanParams& p, cudaStream_t st) {
-    const unsigned grid = (unsigned)(p.units * p.nk);
+template <typename Tin, typename Tout, bool HASB, bool HASZ, bool TMA, bool VEC>
+static cudaError_t bwd_k(const VscanParams& p, const VscanBwdMaps& maps, cudaStream_t st) {
+    const int smem = TMA ? (3 + HASB + HASZ) * kVTokB * 128 : 0;
+    return vscan_launch(vscan_bwd_kernel<Tin, Tout, HASB, HASZ, TMA, VEC>, p, maps, smem, st);
+}
+
+template <typename Tin, typename Tout, bool TMA, bool VEC>
+static cudaError_t bwd_t(const VscanParams& p, const VscanBwdMaps& m, cudaStream_t st) {
     if (p.b)
-        p.z ? vscan_bwd_kernel<Tin, Tout, true, true, VEC><<<grid, 256, 0, st>>>(p)
-            : vscan_bwd_kernel<Tin, Tout, true, false, VEC><<<grid, 256, 0, st>>>(p);
-    else
-        p.z ? vscan_bwd_kernel<Tin, Tout, false, true, VEC><<<grid, 256, 0, st>>>(p)
-            : vscan_bwd_kernel<Tin, Tout, false, false, VEC><<<grid, 256, 0, st>>>(p);
-    return cudaGetLastError();
+        return p.z ? bwd_k<Tin, Tout, true, true, TMA, VEC>(p, m, st)
+                   : bwd_k<Tin, Tout, true, false, TMA, VEC>(p, m, st);
+    return p.z ? bwd_k<Tin, Tout, false, true, TMA, VEC>(p, m, st)
+               : bwd_k<Tin, Tout, false, false, TMA, VEC>(p, m, st);
 }
 
 cudaError_t launch_vscan_bwd(const VscanParams& p, int dtype, int out_dtype, cudaStream_t st) {
     typedef __nv_bfloat16 bf;
-    if (dtype == NAJU_F32) return bwd_t<float, float, true>(p, st);
-    const bool vec = p.d % 2 == 0;
-    if (out_dtype == NAJU_BF16) return vec ? bwd_t<bf, bf, true>(p, st) : bwd_t<bf, bf, false>(p, st);
-    return vec ? bwd_t<bf, float, true>(p, st) : bwd_t<bf, float, false>(p, st);
+    const int64_t Bt = p.units / p.ntiles;
+    VscanBwdMaps m{};
+    if (p.d * (dtype == NAJU_F32 ? 4 : 2) % 16 == 0) {
+        const auto enc = [&](CUtensorMap* map, const void* base) {
+            return !base || vscan_map(map, base, Bt, p.L, p.d, dtype, kVTokB);
+        };
+        if (!(enc(&m.h, p.h) && enc(&m.a, p.a) && enc(&m.b, p.b) && enc(&m.z, p.z) &&
+              enc(&m.dy, p.dy)))
+            return cudaErrorInvalidValue;
+        if (dtype == NAJU_F32) return bwd_t<float, float, true, true>(p, m, st);
+        return out_dtype == NAJU_BF16 ? bwd_t<bf, bf, true, true>(p, m, st)
+                                      : bwd_t<bf, float, true, true>(p, m, st);
+    }
+    if (dtype == NAJU_F32) return bwd_t<float, float, false, true>(p, m, st);
+    if (p.d % 2 == 0)
+        return out_dtype == NAJU_BF16 ? bwd_t<bf, bf, false, true>(p, m, st)
+                                      : bwd_t<bf, float, false, true>(p, m, st);
+    return out_dtype == NAJU_BF16 ? bwd_t<bf, bf, false, false>(p, m, st)
+                                  : bwd_t<bf, float, false, false>(p, m, st);
 }
 
 }  // namespace naju

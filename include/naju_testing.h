@@ -88,6 +88,10 @@ void naju_testing_set_bwd_impl(int32_t impl);
  * sub-chunk kernel, 3 = tensor-core block-form kernel (0 for invalid dims). */
 int32_t naju_testing_bwd_impl(const void* dims);
 
+/* Forces the blocks per unit (cluster size) of the vector-state scan, both
+ * directions: 1, 2, 4, 8 or 16; any other value: automatic. */
+void naju_testing_set_vscan_cluster(int32_t blocks);
+
 /* Self-test of the tensor-core building block of the tensor-core scans:
  * D[128 x N] = A[128 x K] * B[N x K]^T (device pointers, row-major fp32)
  * computed with A in tensor memory, B in shared memory and kind::tf32 MMAs
