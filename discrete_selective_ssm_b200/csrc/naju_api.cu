@@ -613,7 +613,7 @@ int32_t naju_testing_bwd_pieces(const void* dims) {
     return layout(dm).npieces;
 }
 void naju_testing_set_vscan_cluster(int32_t blocks) {
-    g_vcluster = blocks >= 1 && blocks <= 16 && (blocks & (blocks - 1)) == 0 ? blocks : 0;
+    g_vcluster = blocks >= 1 && blocks <= 16 ? blocks : 0;
 }
 void naju_testing_set_sm_count(int32_t sms) { g_sm_override = sms > 0 ? sms : 0; }
 int32_t naju_testing_sm_count(void) { return sm_count(); }

@@ -19,10 +19,10 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
     constexpr int kNT = 2 + (HASB ? 1 : 0) + (HASZ ? 1 : 0);
     typedef Vf<CP> V;
     extern __shared__ __align__(128) unsigned char stage[];  // h, a, [b], [z]
-    __shared__ float2 sagg[2][kVWarps][W];  // (P, X) of each warp's tokens, by round parity
-    __shared__ float sE[2][W];              // the item's entering state
+    __shared__ VPair<CP> sagg[2][kVWarps][32];  // each warp's (P, X), by round parity
+    __shared__ V sE[2][32];                     // the item's entering state
     __shared__ VExchange<CP> ex;
-    __shared__ __align__(8) uint64_t full;
+    __shared__ __align__(8) uint64_t full, empty;  // the stage is filled; has been read
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t cs = p.cluster, rank = cluster_rank();
     const unsigned u = blockIdx.x / cs;
@@ -42,6 +42,7 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
         ex.init();
         if (TMA) {
             mbar_init(&full, 1);
+            mbar_init(&empty, kVWarps);
             fence_proxy_async();
             if ((int)rank < nk) fetch(rank);
         }
@@ -54,7 +55,7 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
         __syncthreads();
 
     if (warp == kVWarps) {  // ------------------------------------- scout
-        float E[CP];
+        V E;
         const int64_t row = bb * p.d + c0;
         const int left = (int)min64(W, p.d - c0);
 #pragma unroll
@@ -65,32 +66,34 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
         bool alive = true;
         for (int i = 0; i < rounds; ++i) {
             const int par = i & 1, k = i * (int)cs + (int)rank;
-            named_bar(1, kVThreads);  // the warps' (P, X) are there, the tiles are read
-            if (TMA && lane == 0 && k + (int)cs < nk) fetch(k + cs);
-            float PC[CP], XC[CP], mine[CP];
-#pragma unroll
-            for (int j = 0; j < CP; ++j) {
-                PC[j] = 1.f, XC[j] = 0.f;
-#pragma unroll
-                for (int w = 0; w < kVWarps; ++w) {
-                    const float2 g = sagg[par][w][lane * CP + j];
-                    PC[j] *= g.x;
-                    XC[j] = fmaf(g.x, XC[j], g.y);
+            if (cs == 1) sE[par][lane] = E;  // known before the item is
+            if (TMA && k + (int)cs < nk) {
+                if (lane == 0) {
+                    if (!mbar_wait(&empty, par, kTmaPolls))
+                        atomicOr(p.status, 1 << NAJU_ERR_TIMEOUT);
+                    fetch(k + cs);
                 }
+                __syncwarp();
             }
+            named_bar(1, kVThreads);         // the warps' (P, X) are there
+            VPair<CP> c = {vset<CP>(1.f), vset<CP>(0.f)};
+#pragma unroll
+            for (int w = 0; w < kVWarps; ++w) {
+                const VPair<CP> g = sagg[par][w][lane];
+                c.P = c.P * g.P;
+                c.X = vfma(g.P, c.X, g.X);
+            }
+            // (a block whose wait ran out sends nothing from then on)
+            if (cs > 1 && alive && !(p.fault_skip_publish && i == 0 && rank == 0))
+                ex.send(i, rank, cs, lane, c);
+            V mine = E;
             if (cs > 1) {
-                ex.round(i, rank, cs, lane, PC, XC, E, mine, alive,
-                         p.fault_skip_publish && i == 0 && rank == 0, p.status, p.wait_limit);
+                mine = ex.fold(i, rank, cs, lane, E, alive, p.status, p.wait_limit);
+                sE[par][lane] = mine;
+                named_arrive(2, kVThreads);
             } else {
-#pragma unroll
-                for (int j = 0; j < CP; ++j) {
-                    mine[j] = E[j];
-                    E[j] = fmaf(PC[j], E[j], XC[j]);
-                }
+                E = vfma(c.P, E, c.X);
             }
-#pragma unroll
-            for (int j = 0; j < CP; ++j) sE[par][lane * CP + j] = mine[j];
-            named_arrive(2, kVThreads);
             if (k < nk) {
                 float* ck = p.ckpt + ((int64_t)u * p.nck + 2 * k) * W;
 #pragma unroll
@@ -132,6 +135,8 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
                         if (HASB) rb[q] = get(2, q);
                         if (HASZ) rz[q] = get(kNT - 1, q);
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty);  // the next tiles may come in
                 } else {
 #pragma unroll
                     for (int q = 0; q < RUN; ++q) {
@@ -152,11 +157,17 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
                 // gates; this warp's (P, X) from a zero state
 #pragma unroll
                 for (int q = 0; q < RUN; ++q) {
-                    V r, s, fc;
-                    gate_rs<Tin>(ra[q], r, s);
-                    gate_sel<Tin>(ra[q], r, s, f[q], fc);
-                    v[q] = (HASB ? vsigm<CP>(VRow<Tin>::unpack(rb[q])) : fc) *
-                           VRow<Tin>::unpack(rh[q]);
+                    V r, s;
+                    if (HASB) {
+                        V r2, s2;
+                        gate_rs2<Tin>(ra[q], rb[q], r, s, r2, s2);
+                        v[q] = gate_sel<Tin>(rb[q], r2, s2);
+                    } else {
+                        gate_rs<Tin>(ra[q], r, s);
+                        v[q] = gate_sel<Tin>(ra[q], s, r);
+                    }
+                    f[q] = gate_sel<Tin>(ra[q], r, s);
+                    v[q] = v[q] * VRow<Tin>::unpack(rh[q]);
                 }
                 if (n < RUN) {  // past the sequence: the identity
 #pragma unroll
@@ -168,23 +179,21 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
                     P = P * f[q];
                     X = vfma(f[q], X, v[q]);
                 }
+            } else if (TMA && lane == 0) {
+                mbar_arrive(&empty);  // (a warp past the sequence's end)
             }
-#pragma unroll
-            for (int j = 0; j < CP; ++j) sagg[par][warp][lane * CP + j] = make_float2(P[j], X[j]);
+            sagg[par][warp][lane] = {P, X};
             named_bar(1, kVThreads);
-            named_bar(2, kVThreads);
-            if (n <= 0) continue;
-            // this warp's entering state, then its tokens
-            V x;
-#pragma unroll
-            for (int j = 0; j < CP; ++j) x[j] = sE[par][lane * CP + j];
+            // the warps before this one, while the exchange goes on
+            VPair<CP> c = {vset<CP>(1.f), vset<CP>(0.f)};
             for (int w = 0; w < warp; ++w) {
-#pragma unroll
-                for (int j = 0; j < CP; ++j) {
-                    const float2 g = sagg[par][w][lane * CP + j];
-                    x[j] = fmaf(g.x, x[j], g.y);
-                }
+                const VPair<CP> g = sagg[par][w][lane];
+                c.P = c.P * g.P;
+                c.X = vfma(g.P, c.X, g.X);
             }
+            if (cs > 1) named_bar(2, kVThreads);
+            if (n <= 0) continue;
+            V x = vfma(c.P, sE[par][lane], c.X);  // this warp's entering state
             if (warp == kVWarps / 2) {  // the checkpoint inside the item
                 float* ck = p.ckpt + ((int64_t)u * p.nck + 2 * k + 1) * W;
 #pragma unroll
@@ -297,10 +306,10 @@ vscan_step_kernel(int64_t n, const T* __restrict__ h, const T* __restrict__ a,
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const uint32_t bits = __float_as_uint(av[k]);
-        Vf<1> r, s, f, fc;
+        Vf<1> r, s;
         gate_rs<float>(bits, r, s);
-        gate_sel<float>(bits, r, s, f, fc);
-        x[k] = fmaf(f.x, x[k], (b ? sigmoidx_(bv[k]) : fc.x) * hv[k]);
+        const float f = gate_sel<float>(bits, r, s).x, fc = gate_sel<float>(bits, s, r).x;
+        x[k] = fmaf(f, x[k], (b ? sigmoidx_(bv[k]) : fc) * hv[k]);
         o[k] = z ? x[k] * (zv[k] * sigmoidx_(zv[k])) : x[k];
     }
     if (m == 8) {

@@ -110,16 +110,35 @@ __device__ __forceinline__ void gate_rs(uint32_t a, Vf<VRow<T>::CP>& r, Vf<VRow<
     for (int j = 0; j < CP; ++j) r[j] = rcpa_(r[j]);
     s = t * r;
 }
+// The same for two logits with one reciprocal: 1 / (Da Db) gives both (the
+// MUFU unit, at 16 lanes a clock, is what bounds the forward; both
+// denominators lie in [1, 2]).
 template <typename T>
-__device__ __forceinline__ void gate_sel(uint32_t a, const Vf<VRow<T>::CP>& r,
-                                         const Vf<VRow<T>::CP>& s, Vf<VRow<T>::CP>& g,
-                                         Vf<VRow<T>::CP>& gc) {
+__device__ __forceinline__ void gate_rs2(uint32_t a, uint32_t b, Vf<VRow<T>::CP>& ra,
+                                         Vf<VRow<T>::CP>& sa, Vf<VRow<T>::CP>& rb,
+                                         Vf<VRow<T>::CP>& sb) {
+    constexpr int CP = VRow<T>::CP;
+    const Vf<CP> one = vset<CP>(1.0f), c = vset<CP>(-kLog2e);
+    Vf<CP> ta = VRow<T>::unpack(a & VRow<T>::kAbs) * c, tb = VRow<T>::unpack(b & VRow<T>::kAbs) * c;
 #pragma unroll
-    for (int j = 0; j < VRow<T>::CP; ++j) {
-        const bool n = VRow<T>::neg(a, j);
-        g[j] = n ? s[j] : r[j];
-        gc[j] = n ? r[j] : s[j];
-    }
+    for (int j = 0; j < CP; ++j) ta[j] = exp2a_(ta[j]), tb[j] = exp2a_(tb[j]);
+    const Vf<CP> da = ta + one, db = tb + one;
+    Vf<CP> r = da * db;
+#pragma unroll
+    for (int j = 0; j < CP; ++j) r[j] = rcpa_(r[j]);
+    ra = r * db;
+    rb = r * da;
+    sa = ta * ra;
+    sb = tb * rb;
+}
+// sigmoid(a) of the two sides (with r and s exchanged: 1 - sigmoid(a)).
+template <typename T>
+__device__ __forceinline__ Vf<VRow<T>::CP> gate_sel(uint32_t a, const Vf<VRow<T>::CP>& r,
+                                                    const Vf<VRow<T>::CP>& s) {
+    Vf<VRow<T>::CP> g;
+#pragma unroll
+    for (int j = 0; j < VRow<T>::CP; ++j) g[j] = VRow<T>::neg(a, j) ? s[j] : r[j];
+    return g;
 }
 // sigmoid alone: 1 / (1 + e^{-v}) saturates cleanly (e^{-v} = inf gives 0).
 template <int CP> __device__ __forceinline__ Vf<CP> vsigm(Vf<CP> v) {
@@ -184,25 +203,25 @@ __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
 }
-// Writes a pair to another block's shared memory and counts its 8 bytes on
-// that block's mbarrier.
-__device__ __forceinline__ void send_pair(uint32_t dst, float a, float b, uint32_t mbar) {
+// A lane's (P, X), and its way to another block's shared memory: the store
+// counts its bytes on that block's mbarrier.
+template <int CP> struct __align__(8 * CP) VPair {
+    Vf<CP> P, X;
+};
+__device__ __forceinline__ void send_pair(uint32_t dst, const VPair<1>& v, uint32_t mbar) {
     asm volatile(
         "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(
             dst),
-        "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(mbar)
+        "r"(__float_as_uint(v.P.x)), "r"(__float_as_uint(v.X.x)), "r"(mbar)
         : "memory");
 }
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* mbar, uint32_t phase) {
-    uint32_t ok;
+__device__ __forceinline__ void send_pair(uint32_t dst, const VPair<2>& v, uint32_t mbar) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(mbar)), "r"(phase)
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, "
+        "[%5];" ::"r"(dst),
+        "r"(__float_as_uint(v.P.x.x)), "r"(__float_as_uint(v.P.x.y)),
+        "r"(__float_as_uint(v.X.x.x)), "r"(__float_as_uint(v.X.x.y)), "r"(mbar)
         : "memory");
-    return ok != 0;
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
@@ -218,12 +237,9 @@ __device__ __forceinline__ void named_arrive(int id, int count) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-// The scout's side of a round's exchange: sends this block's (P, X) to every
-// block, waits (bounded) for all of them and folds them in the order of the
-// items.  On entry E is the round's entering value; returns this block's
-// entering value and leaves the next round's in E.
+// The scout's side of a round's exchange: every block's (P, X) arrives here.
 template <int CP> struct VExchange {
-    float2 pair[2][kVMaxCluster][32 * CP];  // by round parity: every block's (P, X)
+    VPair<CP> pair[2][kVMaxCluster][32];  // by round parity
     uint64_t mbar[2];
 
     __device__ __forceinline__ void init() {
@@ -231,39 +247,35 @@ template <int CP> struct VExchange {
         mbar_init(&mbar[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    __device__ __forceinline__ void round(int i, uint32_t rank, uint32_t cs, int lane,
-                                          const float* P, const float* X, float* E, float* mine,
-                                          bool& alive, bool skip, int* status, long long limit) {
+    __device__ __forceinline__ void send(int i, uint32_t rank, uint32_t cs, int lane,
+                                         const VPair<CP>& v) {
         const int par = i & 1;
-        // (a block whose wait ran out leaves its mbarriers alone from then on)
-        if (lane == 0 && alive) tma::expect_tx(&mbar[par], cs * 32 * CP * 8);
+        if (lane == 0) tma::expect_tx(&mbar[par], cs * 32 * (uint32_t)sizeof(VPair<CP>));
         __syncwarp();
-        if (alive && !skip) {
-            for (uint32_t r = 0; r < cs; ++r) {
-                const uint32_t bar = map_rank(&mbar[par], r);
-                const uint32_t dst = map_rank(&pair[par][rank][lane * CP], r);
-#pragma unroll
-                for (int j = 0; j < CP; ++j) send_pair(dst + 8 * j, P[j], X[j], bar);
-            }
-        }
+#pragma unroll 4
+        for (uint32_t r = 0; r < cs; ++r)
+            send_pair(map_rank(&pair[par][rank][lane], r), v, map_rank(&mbar[par], r));
+    }
+    // Waits (bounded) for all blocks' pairs and folds them in the order of the
+    // items: E, the round's entering value, becomes the next round's; returns
+    // this block's own.
+    __device__ __forceinline__ Vf<CP> fold(int i, uint32_t rank, uint32_t cs, int lane, Vf<CP>& E,
+                                           bool& alive, int* status, long long limit) {
+        const int par = i & 1;
         long long it = 0;
-        while (alive && !mbar_try_wait_cluster(&mbar[par], (i >> 1) & 1)) {
+        while (alive && !mbar_try_wait(&mbar[par], (i >> 1) & 1)) {
             if (++it > limit) alive = false;
         }
         alive = __all_sync(0xffffffffu, alive);
-        if (!alive) {
-            if (lane == 0) atomicOr(status, 1 << NAJU_ERR_TIMEOUT);
-        }
-#pragma unroll
-        for (int j = 0; j < CP; ++j) mine[j] = E[j];
+        if (!alive && lane == 0) atomicOr(status, 1 << NAJU_ERR_TIMEOUT);
+        Vf<CP> mine = E;
+#pragma unroll 4
         for (uint32_t r = 0; r < cs; ++r) {
-#pragma unroll
-            for (int j = 0; j < CP; ++j) {
-                const float2 g = pair[par][r][lane * CP + j];
-                if (r == rank) mine[j] = E[j];
-                E[j] = fmaf(g.x, E[j], g.y);
-            }
+            const VPair<CP> g = pair[par][r][lane];
+            if (r == rank) mine = E;
+            E = vfma(g.P, E, g.X);
         }
+        return mine;
     }
 };
 

@@ -27,10 +27,11 @@ vscan_bwd_kernel(const __grid_constant__ VscanParams p,
     constexpr int kNT = 3 + (HASB ? 1 : 0) + (HASZ ? 1 : 0);
     typedef Vf<CP> V;
     extern __shared__ __align__(128) unsigned char stage[];  // h, a, dy, [b], [z]
-    __shared__ float4 sagg[2][kVWarps][W];  // (P, X, R) of each warp's tokens, by round parity
-    __shared__ float sE[2][W], sA[2][W];    // the item's entering state and adjoint
+    __shared__ VPair<CP> sagg[2][kVWarps][32];  // each warp's (P, X), by round parity
+    __shared__ V srev[2][kVWarps][32];          // and R
+    __shared__ V sE[2][32], sA[2][32];          // the item's entering state and adjoint
     __shared__ VExchange<CP> ex;
-    __shared__ __align__(8) uint64_t full;
+    __shared__ __align__(8) uint64_t full, empty;  // the stage is filled; has been read
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t cs = p.cluster, rank = cluster_rank();
     const unsigned u = blockIdx.x / cs;
@@ -52,6 +53,7 @@ vscan_bwd_kernel(const __grid_constant__ VscanParams p,
         ex.init();
         if (TMA) {
             mbar_init(&full, 1);
+            mbar_init(&empty, kVWarps);
             fence_proxy_async();
             if ((int)rank < nk) fetch(rank);
         }
@@ -63,7 +65,7 @@ vscan_bwd_kernel(const __grid_constant__ VscanParams p,
         __syncthreads();
 
     if (warp == kVWarps) {  // ------------------------------------- scout
-        float A[CP], E0[CP];
+        V A, E0;
         const int64_t row = bb * p.d + c0;
         const int left = (int)min64(W, p.d - c0);
         const auto state = [&](int o) {  // the checkpoint at the start of item o
@@ -82,35 +84,34 @@ vscan_bwd_kernel(const __grid_constant__ VscanParams p,
         bool alive = true;
         for (int i = 0; i < rounds; ++i) {
             const int par = i & 1, o = i * (int)cs + (int)rank;
-#pragma unroll
-            for (int j = 0; j < CP; ++j) sE[par][lane * CP + j] = E0[j];
+            sE[par][lane] = E0;
+            if (cs == 1) sA[par][lane] = A;  // known before the item is
             state(o + (int)cs);
-            named_bar(1, kVThreads);  // the warps' sums are there, the tiles are read
-            if (TMA && lane == 0 && o + (int)cs < nk) fetch(o + cs);
-            float PC[CP], RC[CP], mine[CP];
-#pragma unroll
-            for (int j = 0; j < CP; ++j) {
-                PC[j] = 1.f, RC[j] = 0.f;
-#pragma unroll
-                for (int w = kVWarps - 1; w >= 0; --w) {
-                    const float4 g = sagg[par][w][lane * CP + j];
-                    PC[j] *= g.x;
-                    RC[j] = fmaf(g.x, RC[j], g.z);
+            if (TMA && o + (int)cs < nk) {
+                if (lane == 0) {
+                    if (!mbar_wait(&empty, par, kTmaPolls))
+                        atomicOr(p.status, 1 << NAJU_ERR_TIMEOUT);
+                    fetch(o + cs);
                 }
+                __syncwarp();
             }
+            named_bar(1, kVThreads);  // the warps' sums are there
+            VPair<CP> c = {vset<CP>(1.f), vset<CP>(0.f)};
+#pragma unroll
+            for (int w = kVWarps - 1; w >= 0; --w) {
+                const V g = sagg[par][w][lane].P;
+                c.P = c.P * g;
+                c.X = vfma(g, c.X, srev[par][w][lane]);
+            }
+            // (a block whose wait ran out sends nothing from then on)
+            if (cs > 1 && alive && !(p.fault_skip_publish && i == 0 && rank == 0))
+                ex.send(i, rank, cs, lane, c);
             if (cs > 1) {
-                ex.round(i, rank, cs, lane, PC, RC, A, mine, alive,
-                         p.fault_skip_publish && i == 0 && rank == 0, p.status, p.wait_limit);
+                sA[par][lane] = ex.fold(i, rank, cs, lane, A, alive, p.status, p.wait_limit);
+                named_arrive(2, kVThreads);
             } else {
-#pragma unroll
-                for (int j = 0; j < CP; ++j) {
-                    mine[j] = A[j];
-                    A[j] = fmaf(PC[j], A[j], RC[j]);
-                }
+                A = vfma(c.P, A, c.X);
             }
-#pragma unroll
-            for (int j = 0; j < CP; ++j) sA[par][lane * CP + j] = mine[j];
-            named_arrive(2, kVThreads);
         }
         if (rank == 0 && p.dx0) {
 #pragma unroll
@@ -152,6 +153,8 @@ vscan_bwd_kernel(const __grid_constant__ VscanParams p,
                         if (HASB) rb[q] = get(3, q);
                         if (HASZ) rz[q] = get(kNT - 1, q);
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty);  // the next tiles may come in
                 } else {
 #pragma unroll
                     for (int q = 0; q < RUN; ++q) {
@@ -174,19 +177,20 @@ vscan_bwd_kernel(const __grid_constant__ VscanParams p,
 #pragma unroll
                 for (int q = 0; q < RUN; ++q) {
                     const V h = VRow<Tin>::unpack(rh[q]), dy = VRow<Tin>::unpack(rd[q]);
-                    V r, s, fc;
-                    gate_rs<Tin>(ra[q], r, s);
-                    gate_sel<Tin>(ra[q], r, s, f[q], fc);
-                    m[q] = r * s;
+                    V r, s;
                     if (HASB) {
-                        gate_rs<Tin>(rb[q], r, s);
-                        V ic;
-                        gate_sel<Tin>(rb[q], r, s, gi[q], ic);
-                        w[q] = h * (r * s);
+                        V r2, s2;
+                        gate_rs2<Tin>(ra[q], rb[q], r, s, r2, s2);
+                        gi[q] = gate_sel<Tin>(rb[q], r2, s2);
+                        w[q] = h * (r2 * s2);
+                        m[q] = r * s;
                     } else {
-                        gi[q] = fc;
+                        gate_rs<Tin>(ra[q], r, s);
+                        gi[q] = gate_sel<Tin>(ra[q], s, r);
+                        m[q] = r * s;
                         w[q] = m[q] * h * minus;
                     }
+                    f[q] = gate_sel<Tin>(ra[q], r, s);
                     v[q] = gi[q] * h;
                     if (HASZ) {
                         const V z = VRow<Tin>::unpack(rz[q]);
@@ -209,41 +213,36 @@ vscan_bwd_kernel(const __grid_constant__ VscanParams p,
                     const int rq = RUN - 1 - q;
                     R = f[rq] * (dx[rq] + R);
                 }
+            } else if (TMA && lane == 0) {
+                mbar_arrive(&empty);  // (a warp past the sequence's end)
             }
-#pragma unroll
-            for (int j = 0; j < CP; ++j)
-                sagg[par][warp][lane * CP + j] = make_float4(P[j], X[j], R[j], 0.f);
+            sagg[par][warp][lane] = {P, X};
+            srev[par][warp][lane] = R;
             named_bar(1, kVThreads);
-            // the states need no exchange: they go before the second barrier
-            V xs[RUN + 1], r;
+            // what needs no exchange goes before the second barrier: the
+            // states, and the sums of the warps behind this one
+            VPair<CP> c = {one, vset<CP>(0.f)};
             if (n > 0) {
-#pragma unroll
-                for (int j = 0; j < CP; ++j) xs[0][j] = sE[par][lane * CP + j];
+                V x = sE[par][lane];
                 for (int o = 0; o < warp; ++o) {
-#pragma unroll
-                    for (int j = 0; j < CP; ++j) {
-                        const float4 g = sagg[par][o][lane * CP + j];
-                        xs[0][j] = fmaf(g.x, xs[0][j], g.y);
-                    }
+                    const VPair<CP> g = sagg[par][o][lane];
+                    x = vfma(g.P, x, g.X);
                 }
 #pragma unroll
                 for (int q = 0; q < RUN; ++q) {
-                    xs[q + 1] = vfma(f[q], xs[q], v[q]);
-                    m[q] = HASB ? m[q] * xs[q] : vfma(m[q], xs[q], w[q]);  // da / g
-                    if (HASZ) e[q] = e[q] * xs[q + 1];                     // dz
+                    m[q] = HASB ? m[q] * x : vfma(m[q], x, w[q]);  // da / g
+                    x = vfma(f[q], x, v[q]);
+                    if (HASZ) e[q] = e[q] * x;                     // dz
+                }
+                for (int o = kVWarps - 1; o > warp; --o) {
+                    const V g = sagg[par][o][lane].P;
+                    c.P = c.P * g;
+                    c.X = vfma(g, c.X, srev[par][o][lane]);
                 }
             }
-            named_bar(2, kVThreads);
+            if (cs > 1) named_bar(2, kVThreads);
             if (n <= 0) continue;
-#pragma unroll
-            for (int j = 0; j < CP; ++j) r[j] = sA[par][lane * CP + j];
-            for (int o = kVWarps - 1; o > warp; --o) {
-#pragma unroll
-                for (int j = 0; j < CP; ++j) {
-                    const float4 g = sagg[par][o][lane * CP + j];
-                    r[j] = fmaf(g.x, r[j], g.z);
-                }
-            }
+            V r = vfma(c.P, sA[par][lane], c.X);  // the adjoint entering from behind
             const auto at = [&](void* t, int q) {
                 return reinterpret_cast<Tout*>(
                     reinterpret_cast<char*>(static_cast<Tout*>(t) + tile) + (off0 + q * stride));

@@ -89,7 +89,7 @@ void naju_testing_set_bwd_impl(int32_t impl);
 int32_t naju_testing_bwd_impl(const void* dims);
 
 /* Forces the blocks per unit (cluster size) of the vector-state scan, both
- * directions: 1, 2, 4, 8 or 16; any other value: automatic. */
+ * directions: 1 to 16; any other value: automatic. */
 void naju_testing_set_vscan_cluster(int32_t blocks);
 
 /* Self-test of the tensor-core building block of the tensor-core scans:
