@@ -100,7 +100,11 @@ def lib(build_if_missing: bool = True):
             L.naju_vscan_fwd.argtypes = [dp] + [vp] * 8 + [sz, vp]
             L.naju_vscan_bwd.argtypes = [dp] + [vp] * 12 + [sz, vp]
             L.naju_vscan_step.argtypes = [i64, i64, i32] + [vp] * 7
-            for name in ("naju_vscan_fwd", "naju_vscan_bwd", "naju_vscan_step",
+            L.naju_state_store.argtypes = [i64] * 4 + [vp] * 5
+            L.naju_state_load.argtypes = [i64] * 4 + [vp] * 5
+            L.naju_w4_quantize.argtypes = [i64] * 2 + [i32] * 2 + [vp] * 4
+            L.naju_w4_linear.argtypes = [i64] * 3 + [i32] * 2 + [vp] * 7
+            for name in ("naju_w4_quantize", "naju_w4_linear", "naju_state_store", "naju_state_load", "naju_vscan_fwd", "naju_vscan_bwd", "naju_vscan_step",
                          "naju_conv_silu_fwd", "naju_conv_silu_bwd", "naju_scan_fwd",
                          "naju_scan_bwd", "naju_scan_step", "naju_conv_silu_step",
                          "naju_scan_step_conv", "naju_last_device_status"):
@@ -429,6 +433,96 @@ def vscan_step(state, h, a, b=None, z=None, y=None, stream=None):
             _arg(state, "state", sh, torch.float32, dev), _arg(y, "y", sh, dt, dev))
     _launch(dev, stream, lambda s: L.naju_vscan_step(*args, s), "naju_vscan_step")
     return y
+
+
+# ------------------------------------------------------ 4-bit projections
+def _w4_group(group: int):
+    if group not in (32, 64, 128):
+        raise NajuError(2, f"4-bit projection with groups of {group}")
+
+
+def w4_quantize(W, group=128, stream=None):
+    """Quantises a projection W [n_out, n_in] to 4 bits a weight with one bf16
+    scale per `group` (32, 64 or 128) inputs.  Returns (wq, scales): uint8
+    [n_out, ceil(n_in / 128) * 64] in w4_linear's packed order, and bf16
+    [n_out, ceil(n_in / group)]."""
+    if W.dim() != 2:
+        raise ValueError(f"W must be [n_out, n_in], got {tuple(W.shape)}")
+    _w4_group(group)
+    dev, (O, K) = W.device, W.shape
+    w = _arg(W, "W", W.shape, W.dtype, dev)
+    wq = torch.empty((O, -(-K // 128) * 64), dtype=torch.uint8, device=dev)
+    scales = torch.empty((O, -(-K // group)), dtype=torch.bfloat16, device=dev)
+    args = (O, K, group, _dt(W), w, wq.data_ptr(), scales.data_ptr())
+    L = lib()
+    _launch(dev, stream, lambda s: L.naju_w4_quantize(*args, s), "naju_w4_quantize")
+    return wq, scales
+
+
+def w4_linear(x, wq, scales, group=128, bias=None, residual=None, y=None, stream=None):
+    """y = x W^T (+ bias) (+ residual) with the 4-bit W of w4_quantize:
+    x [..., n_in] (its leading dimensions are rows), bias [n_out] fp32, residual
+    and y [..., n_out] in x's dtype."""
+    _w4_group(group)
+    dev, dt, K = x.device, x.dtype, x.shape[-1]
+    O = wq.shape[0]
+    out = x.shape[:-1] + (O,)
+    if y is None:
+        y = torch.empty(out, dtype=dt, device=dev)
+    m = x.numel() // K if K else 0
+    args = (m, K, O, group, _dt(x), _arg(x, "x", x.shape, dt, dev),
+            _arg(wq, "wq", (O, -(-K // 128) * 64), torch.uint8, dev),
+            _arg(scales, "scales", (O, -(-K // group)), torch.bfloat16, dev),
+            _arg(bias, "bias", (O,), torch.float32, dev),
+            _arg(residual, "residual", out, dt, dev), _arg(y, "y", out, dt, dev))
+    L = lib()
+    _launch(dev, stream, lambda s: L.naju_w4_linear(*args, s), "naju_w4_linear")
+    return y
+
+
+# -------------------------------------------------------- 8-bit state cache
+def state_pool(n_slots: int, d_inner: int, d_state: int, device):
+    """An empty pool for parked decode states: (pool_q int8, pool_scale fp32);
+    every slot reads back as a zero state."""
+    return (torch.zeros((n_slots, d_inner, d_state), dtype=torch.int8, device=device),
+            torch.zeros((n_slots, d_inner), dtype=torch.float32, device=device))
+
+
+def _cache_args(pool_q, pool_scale, slots):
+    if pool_q.dim() != 3:
+        raise ValueError(f"pool_q must be [n_slots, d_inner, d_state], got {tuple(pool_q.shape)}")
+    if slots.dim() != 1:
+        raise ValueError(f"slots must be [n], got {tuple(slots.shape)}")
+    (S, d, N), dev = pool_q.shape, pool_q.device
+    n = slots.shape[0]
+    return ((n, d, N, S), dev, _arg(pool_q, "pool_q", pool_q.shape, torch.int8, dev),
+            _arg(pool_scale, "pool_scale", pool_q.shape[:2], torch.float32, dev),
+            _arg(slots, "slots", slots.shape, torch.int32, dev))
+
+
+def state_store(state, slots, pool_q, pool_scale, stream=None):
+    """Parks decode states: batch place i of `state` [n, d_inner, d_state] fp32
+    into slot slots[i] (int32) of the pool, 8 bits a value with one scale per
+    row.  Slots outside the pool store nothing; of places that name the same
+    slot the last is stored."""
+    sizes, dev, q, sc, sl = _cache_args(pool_q, pool_scale, slots)
+    st = _arg(state, "state", sizes[:3], torch.float32, dev)
+    L = lib()
+    _launch(dev, stream, lambda s: L.naju_state_store(*sizes, st, sl, q, sc, s),
+            "naju_state_store")
+
+
+def state_load(pool_q, pool_scale, slots, state=None, stream=None):
+    """Resumes parked states: slot slots[i] into batch place i.  Slots outside
+    the pool give a zero state.  Returns state [n, d_inner, d_state] fp32."""
+    sizes, dev, q, sc, sl = _cache_args(pool_q, pool_scale, slots)
+    if state is None:
+        state = torch.empty(sizes[:3], dtype=torch.float32, device=dev)
+    st = _arg(state, "state", sizes[:3], torch.float32, dev)
+    L = lib()
+    _launch(dev, stream, lambda s: L.naju_state_load(*sizes, q, sc, sl, st, s),
+            "naju_state_load")
+    return state
 
 
 def last_device_status(workspace, stream=None) -> int:

@@ -252,6 +252,7 @@ Layout layout(const naju_dims* dm) {
 // Vector-state scan: workspace layout (status word, checkpoints).
 struct VLayout {
     int64_t ntiles, units, nkf, nkb;  // items per unit, forward and backward
+    int64_t nck;                      // checkpoints per unit, padded to whole forward items
     size_t off_ckpt, total;
 };
 VLayout vlayout(const naju_dims* dm) {
@@ -261,16 +262,26 @@ VLayout vlayout(const naju_dims* dm) {
     l.units = dm->batch * l.ntiles;
     l.nkf = cdiv(dm->seqlen, vscan_tokens());
     l.nkb = cdiv(dm->seqlen, vscan_tokens_bwd());
+    l.nck = l.nkf * (vscan_tokens() / vscan_tokens_bwd());
     l.off_ckpt = 256;
-    l.total = up256(l.off_ckpt + sizeof(float) * 2 * (size_t)(l.units * l.nkf) * tile);
+    l.total = up256(l.off_ckpt + sizeof(float) * (size_t)(l.units * l.nck) * tile);
     return l;
 }
 
-// Blocks per unit of the vector-state scan.
+// Blocks per unit of the vector-state scan: enough for one and a half times
+// the blocks that run at once (`slots`), so that the last wave is short, and
+// no more, since every exchange grows with them; more than the portable eight
+// only where all units together are still few.  Measured (bf16, forward /
+// backward us at 1, 2, 4, 8 blocks): 512 units of 4096 tokens 285, 256, 277,
+// 322 / 582, 572, 583, 620; 192 units of 2048 tokens 80, 62, 65, 73 / 138,
+// 134, 120, 131; 32 units of 65536 tokens 1630, 951, 482, 353 / 3078, 1619,
+// 901, 601 (twelve to sixteen blocks: 398 and more / 758 and more, those
+// clusters fill the GPU's processor groups unevenly); one unit of 65536
+// tokens 250 at eight, 143 at sixteen.
 int vscan_cluster(int64_t units, int64_t nk, int slots) {
     if (g_vcluster > 0) return g_vcluster;
     int cs = 1;
-    while (cs < 8 && cs < nk && units * cs < 4LL * slots) cs *= 2;
+    while (cs < 8 && cs < nk && 2 * units * cs < 3LL * slots) cs *= 2;
     if (cs == 8 && nk > 8 && units * 16 <= slots) cs = 16;
     return cs;
 }
@@ -325,7 +336,7 @@ void vscan_params(VscanParams& p, const naju_dims* dims, const VLayout& l, char*
     p.status = reinterpret_cast<int*>(ws);
     p.ckpt = reinterpret_cast<float*>(ws + l.off_ckpt);
     p.L = dims->seqlen; p.d = dims->d_inner;
-    p.units = l.units; p.nck = 2 * l.nkf; p.ntiles = (int)l.ntiles;
+    p.units = l.units; p.nck = l.nck; p.ntiles = (int)l.ntiles;
     p.wait_limit = g_wait_limit;
     p.fault_skip_publish = g_skip_publish;
 }
@@ -568,6 +579,66 @@ naju_status naju_vscan_step(int64_t batch, int64_t d_inner, int32_t dtype, const
     NAJU_REQUIRE(ok_act(h) && ok_act(a) && ok_opt(b) && ok_opt(z) && ok_act(state) && ok_act(y));
     return cuda_status(launch_vscan_step(batch * d_inner, h, a, b, z, state, y, dtype,
                                          static_cast<cudaStream_t>(stream)));
+}
+
+static naju_status check_w4(int64_t n_in, int64_t n_out, int32_t group, int32_t dtype) {
+    if (n_in < 1 || n_out < 1 || n_in > (1 << 24) || n_out > (1 << 24)) return NAJU_ERR_INVALID_ARG;
+    if (group != 32 && group != 64 && group != 128) return NAJU_ERR_UNSUPPORTED;
+    if (dtype != NAJU_F32 && dtype != NAJU_BF16) return NAJU_ERR_UNSUPPORTED;
+    return NAJU_OK;
+}
+
+naju_status naju_w4_quantize(int64_t n_out, int64_t n_in, int32_t group, int32_t dtype,
+                             const void* W, void* wq, void* scales, void* stream) {
+    const naju_status st = check_w4(n_in, n_out, group, dtype);
+    if (st != NAJU_OK) return st;
+    NAJU_REQUIRE(W && aligned(W, dtype == NAJU_F32 ? 4 : 2) && ok_act(wq) && scales &&
+                 aligned(scales, 2));
+    NAJU_REQUIRE(n_out * cdiv(n_in, 128) <= (1LL << 32));
+    return cuda_status(launch_w4_quantize(n_out, n_in, group, dtype, W, wq, scales,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+naju_status naju_w4_linear(int64_t m, int64_t n_in, int64_t n_out, int32_t group, int32_t dtype,
+                           const void* x, const void* wq, const void* scales, const float* bias,
+                           const void* residual, void* y, void* stream) {
+    const naju_status st = check_w4(n_in, n_out, group, dtype);
+    if (st != NAJU_OK) return st;
+    NAJU_REQUIRE(m >= 1 && m <= (1 << 20));
+    NAJU_REQUIRE(ok_act(x) && ok_act(wq) && scales && aligned(scales, 2) && ok_act(y));
+    NAJU_REQUIRE(ok_opt(residual) && (!bias || aligned(bias, 4)));
+    return cuda_status(launch_w4_linear(m, n_in, n_out, group, dtype, x, wq, scales, bias,
+                                        residual, y, sm_count(),
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+static naju_status check_cache(int64_t n, int64_t d, int64_t N, int64_t n_slots) {
+    if (n < 1 || n > 65535 || d < 1 || d > (1 << 20) || n_slots < 1 || n_slots > (1LL << 31) - 1)
+        return NAJU_ERR_INVALID_ARG;
+    if (N != 16 && N != 32 && N != 64 && N != 128) return NAJU_ERR_UNSUPPORTED;
+    return NAJU_OK;
+}
+
+naju_status naju_state_store(int64_t n, int64_t d_inner, int64_t d_state, int64_t n_slots,
+                             const float* state, const int32_t* slots, int8_t* pool_q,
+                             float* pool_scale, void* stream) {
+    const naju_status st = check_cache(n, d_inner, d_state, n_slots);
+    if (st != NAJU_OK) return st;
+    NAJU_REQUIRE(ok_act(state) && ok_act(pool_q) && pool_scale && aligned(pool_scale, 4) &&
+                 slots && aligned(slots, 4));
+    return cuda_status(launch_state_store(n, d_inner, d_state, n_slots, state, slots, pool_q,
+                                          pool_scale, static_cast<cudaStream_t>(stream)));
+}
+
+naju_status naju_state_load(int64_t n, int64_t d_inner, int64_t d_state, int64_t n_slots,
+                            const int8_t* pool_q, const float* pool_scale, const int32_t* slots,
+                            float* state, void* stream) {
+    const naju_status st = check_cache(n, d_inner, d_state, n_slots);
+    if (st != NAJU_OK) return st;
+    NAJU_REQUIRE(ok_act(state) && ok_act(pool_q) && pool_scale && aligned(pool_scale, 4) &&
+                 slots && aligned(slots, 4));
+    return cuda_status(launch_state_load(n, d_inner, d_state, n_slots, pool_q, pool_scale, slots,
+                                         state, static_cast<cudaStream_t>(stream)));
 }
 
 naju_status naju_last_device_status(void* workspace, void* stream) {

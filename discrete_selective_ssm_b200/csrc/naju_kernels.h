@@ -155,7 +155,7 @@ struct VscanParams {
     float* ckpt;            // [units][nck][tile]: state at every backward item's start
     int64_t L, d;
     int64_t units, nk;      // batch * channel tiles; this direction's items per unit
-    int64_t nck;            // checkpoints per unit (two per forward item)
+    int64_t nck;            // checkpoints per unit
     int ntiles;
     int cluster;            // blocks that share a unit
     long long wait_limit;
@@ -164,11 +164,27 @@ struct VscanParams {
 int vscan_tile(int dtype);  // channels per item
 int vscan_tokens();         // tokens per forward item
 int vscan_tokens_bwd();     // tokens per backward item and checkpoint
+bool vscan_tma(int64_t d, int dtype);
 bool vscan_map(CUtensorMap* map, const void* base, int64_t Bt, int64_t L, int64_t d, int dtype,
                int rows);
 cudaError_t launch_vscan_fwd(const VscanParams& p, int dtype, int out_dtype, cudaStream_t st);
 cudaError_t launch_vscan_bwd(const VscanParams& p, int dtype, int out_dtype, cudaStream_t st);
 cudaError_t launch_vscan_step(int64_t n, const void* h, const void* a, const void* b,
                               const void* z, float* state, void* y, int dtype, cudaStream_t st);
+
+// ------------------------------------------------------ 4-bit projections
+cudaError_t launch_w4_quantize(int64_t n_out, int64_t n_in, int group, int dtype, const void* W,
+                               void* wq, void* scales, cudaStream_t st);
+cudaError_t launch_w4_linear(int64_t m, int64_t n_in, int64_t n_out, int group, int dtype,
+                             const void* x, const void* wq, const void* scales, const float* bias,
+                             const void* residual, void* y, int sms, cudaStream_t st);
+
+// -------------------------------------------------------- 8-bit state cache
+cudaError_t launch_state_store(int64_t n, int64_t d, int64_t N, int64_t n_slots,
+                               const float* state, const int* slots, int8_t* pool_q,
+                               float* pool_scale, cudaStream_t st);
+cudaError_t launch_state_load(int64_t n, int64_t d, int64_t N, int64_t n_slots,
+                              const int8_t* pool_q, const float* pool_scale, const int* slots,
+                              float* state, cudaStream_t st);
 
 }  // namespace naju

@@ -95,7 +95,7 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
                 E = vfma(c.P, E, c.X);
             }
             if (k < nk) {
-                float* ck = p.ckpt + ((int64_t)u * p.nck + 2 * k) * W;
+                float* ck = p.ckpt + ((int64_t)u * p.nck + (int64_t)k * (kVTokF / kVTokB)) * W;
 #pragma unroll
                 for (int j = 0; j < CP; ++j) ck[vchan<CP, VEC>(lane, j)] = mine[j];
             }
@@ -194,8 +194,9 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
             if (cs > 1) named_bar(2, kVThreads);
             if (n <= 0) continue;
             V x = vfma(c.P, sE[par][lane], c.X);  // this warp's entering state
-            if (warp == kVWarps / 2) {  // the checkpoint inside the item
-                float* ck = p.ckpt + ((int64_t)u * p.nck + 2 * k + 1) * W;
+            if (warp > 0 && warp * RUN % kVTokB == 0) {  // a checkpoint inside the item
+                float* ck = p.ckpt + ((int64_t)u * p.nck + (int64_t)k * (kVTokF / kVTokB) +
+                                      warp * RUN / kVTokB) * W;
 #pragma unroll
                 for (int j = 0; j < CP; ++j) ck[vchan<CP, VEC>(lane, j)] = x[j];
             }
@@ -247,11 +248,14 @@ bool vscan_map(CUtensorMap* map, const void* base, int64_t Bt, int64_t L, int64_
     return tma_encode_bf16_3d(map, base, Bt, L, dtype == NAJU_F32 ? 2 * d : d, rows, 64);
 }
 
+// Whether rows start on TMA's 16 bytes.
+bool vscan_tma(int64_t d, int dtype) { return d * (dtype == NAJU_F32 ? 4 : 2) % 16 == 0; }
+
 cudaError_t launch_vscan_fwd(const VscanParams& p, int dtype, int out_dtype, cudaStream_t st) {
     typedef __nv_bfloat16 bf;
     const int64_t Bt = p.units / p.ntiles;
     VscanMaps m{};
-    if (p.d * (dtype == NAJU_F32 ? 4 : 2) % 16 == 0) {
+    if (vscan_tma(p.d, dtype)) {
         const auto enc = [&](CUtensorMap* map, const void* base) {
             return !base || vscan_map(map, base, Bt, p.L, p.d, dtype, kVTokF);
         };

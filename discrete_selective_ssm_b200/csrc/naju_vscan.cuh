@@ -36,7 +36,7 @@ using namespace tc;
 
 constexpr int kVWarps = 8;                      // compute warps
 constexpr int kVThreads = 32 * (kVWarps + 1);
-constexpr int kVRunF = 8, kVRunB = 4;           // tokens per warp and item
+constexpr int kVRunF = 8, kVRunB = 4;           // tokens per warp and item, forward, backward
 constexpr int kVTokF = kVWarps * kVRunF;        // tokens per forward item
 constexpr int kVTokB = kVWarps * kVRunB;        // per backward item, and per checkpoint
 

@@ -219,8 +219,12 @@ vscan_bwd_kernel(const __grid_constant__ VscanParams p,
             sagg[par][warp][lane] = {P, X};
             srev[par][warp][lane] = R;
             named_bar(1, kVThreads);
+            const auto at = [&](void* t, int q) {
+                return reinterpret_cast<Tout*>(
+                    reinterpret_cast<char*>(static_cast<Tout*>(t) + tile) + (off0 + q * stride));
+            };
             // what needs no exchange goes before the second barrier: the
-            // states, and the sums of the warps behind this one
+            // states with dz, and the sums of the warps behind this one
             VPair<CP> c = {one, vset<CP>(0.f)};
             if (n > 0) {
                 V x = sE[par][lane];
@@ -232,7 +236,7 @@ vscan_bwd_kernel(const __grid_constant__ VscanParams p,
                 for (int q = 0; q < RUN; ++q) {
                     m[q] = HASB ? m[q] * x : vfma(m[q], x, w[q]);  // da / g
                     x = vfma(f[q], x, v[q]);
-                    if (HASZ) e[q] = e[q] * x;                     // dz
+                    if (HASZ && q < n) vstore<Tout, CP, VEC>(at(p.dz, q), left, e[q] * x);
                 }
                 for (int o = kVWarps - 1; o > warp; --o) {
                     const V g = sagg[par][o][lane].P;
@@ -243,17 +247,12 @@ vscan_bwd_kernel(const __grid_constant__ VscanParams p,
             if (cs > 1) named_bar(2, kVThreads);
             if (n <= 0) continue;
             V r = vfma(c.P, sA[par][lane], c.X);  // the adjoint entering from behind
-            const auto at = [&](void* t, int q) {
-                return reinterpret_cast<Tout*>(
-                    reinterpret_cast<char*>(static_cast<Tout*>(t) + tile) + (off0 + q * stride));
-            };
             const auto token = [&](int q) {
                 const V g = dx[q] + r;
                 r = f[q] * g;
                 vstore<Tout, CP, VEC>(at(p.dh, q), left, g * gi[q]);
                 vstore<Tout, CP, VEC>(at(p.da, q), left, g * m[q]);
                 if (HASB) vstore<Tout, CP, VEC>(at(p.db, q), left, g * w[q]);
-                if (HASZ) vstore<Tout, CP, VEC>(at(p.dz, q), left, e[q]);
             };
             if (n == RUN) {
 #pragma unroll
@@ -291,7 +290,7 @@ cudaError_t launch_vscan_bwd(const VscanParams& p, int dtype, int out_dtype, cud
     typedef __nv_bfloat16 bf;
     const int64_t Bt = p.units / p.ntiles;
     VscanBwdMaps m{};
-    if (p.d * (dtype == NAJU_F32 ? 4 : 2) % 16 == 0) {
+    if (vscan_tma(p.d, dtype)) {
         const auto enc = [&](CUtensorMap* map, const void* base) {
             return !base || vscan_map(map, base, Bt, p.L, p.d, dtype, kVTokB);
         };

@@ -219,6 +219,54 @@ naju_status naju_vscan_step(int64_t batch, int64_t d_inner, int32_t dtype, const
                             const void* a, const void* b, const void* z, float* state, void* y,
                             void* stream);
 
+/* ---- 4-bit projections (the block's matrices, for decoding a few sessions).
+ * A weight is W[o, k] = scale[o, k / group] (q[o, k] - 8) with q in 0..15 and
+ * one bf16 scale per `group` (32, 64 or 128) consecutive inputs of a row;
+ * scales are [n_out, ceil(n_in / group)].  wq is [n_out, ceil(n_in / 128) * 64]
+ * bytes: each row in blocks of 128 inputs (inputs past n_in hold q = 8), a
+ * block as 16 little-endian 32-bit words; word 4 c + j holds inputs
+ * 32 j + 8 c .. + 7, the even ones in nibbles 0..3, the odd ones in nibbles
+ * 4..7 (nibble 0 lowest).  wq must be 16-byte, scales 2-byte aligned. */
+
+/* Quantises W [n_out, n_in] (row-major, `dtype`) to that form: per group
+ * scale = bf16(max|w| / 7), q = 8 + round(w / scale) clamped to 0..15.  A
+ * group that is all zero has scale 0 and q = 8; one with an infinity or a NaN
+ * gets a NaN scale. */
+naju_status naju_w4_quantize(int64_t n_out, int64_t n_in, int32_t group, int32_t dtype,
+                             const void* W, void* wq, void* scales, void* stream);
+
+/* y = x W^T (+ bias) (+ residual): x [m, n_in], y and residual [m, n_out] in
+ * `dtype`, bias [n_out] fp32; bias and residual may be NULL, residual may be
+ * y itself.  Sums are fp32 and every product is exact (bf16 x) or exact to
+ * 2^-24 of it (fp32 x); y is rounded once.  m is at most 2^20, but the
+ * weights are read again for every 64 rows of x: meant for m up to a few
+ * hundred.  Uses no workspace. */
+naju_status naju_w4_linear(int64_t m, int64_t n_in, int64_t n_out, int32_t group, int32_t dtype,
+                           const void* x, const void* wq, const void* scales, const float* bias,
+                           const void* residual, void* y, void* stream);
+
+/* ---- 8-bit cache of decode states: sessions that pause are parked in a pool
+ * of slots, a quarter of the fp32 state's size, and resumed in any batch
+ * place.  pool_q [n_slots, d_inner, d_state] int8, pool_scale [n_slots,
+ * d_inner] fp32; a row of d_state (16, 32, 64 or 128) values has
+ * scale = fp32(max|x| / 127) and q = the exact quotient x / scale rounded to
+ * nearest, ties to even (at most 127 in size, where a scale below the normal
+ * range is itself coarse); it reads back as scale * q.  A row with an
+ * infinity or a NaN reads back as NaN throughout. */
+
+/* Stores state [n, d_inner, d_state] fp32: batch place i into slot slots[i]
+ * (device int32 [n]).  A slot outside [0, n_slots) stores nothing; where a
+ * slot is named more than once the last place with it is the one stored. */
+naju_status naju_state_store(int64_t n, int64_t d_inner, int64_t d_state, int64_t n_slots,
+                             const float* state, const int32_t* slots, int8_t* pool_q,
+                             float* pool_scale, void* stream);
+
+/* Loads slot slots[i] into batch place i of state; a slot outside
+ * [0, n_slots) gives a zero state (a new session). */
+naju_status naju_state_load(int64_t n, int64_t d_inner, int64_t d_state, int64_t n_slots,
+                            const int8_t* pool_q, const float* pool_scale, const int32_t* slots,
+                            float* state, void* stream);
+
 /* Synchronises `stream`, reads the workspace's status word (NAJU_OK or
  * NAJU_ERR_TIMEOUT) and clears it.  Returns NAJU_ERR_CUDA if the stream
  * itself reports an error. */

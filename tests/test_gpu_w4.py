@@ -1,0 +1,205 @@
+"""The 4-bit projections against the definition in 64 bits.
+
+Bound, element by element: every product (q - 8) x is exact, a group's sum of G
+of them and the sum over groups round by at most half a step (u = 2^-24) per
+addition, and the tensor cores' own additions by at most a whole one; so y is
+off by at most 2 u (n_in + 4) of the sum of |terms|.  A bf16 y adds half a
+bf16 step, 2^-8 of the value.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import discrete_selective_ssm_b200 as naju
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def unpack(wq, K):
+    """q [n_out, K] from the packed words, word by word."""
+    w = wq.cpu().numpy().view("<u4")
+    O = w.shape[0]
+    q = np.zeros((O, w.shape[1] // 16 * 128), dtype=np.int64)
+    for b in range(w.shape[1] // 16):
+        for c in range(4):
+            for j in range(4):
+                word = w[:, 16 * b + 4 * c + j]
+                for e in range(8):
+                    nibble = e // 2 + 4 * (e % 2)
+                    q[:, 128 * b + 32 * j + 8 * c + e] = (word >> np.uint32(4 * nibble)) & 15
+    assert (q[:, K:] == 8).all()
+    return q[:, :K]
+
+
+def weights(wq, scales, K, G):
+    s = np.repeat(scales.double().cpu().numpy(), G, 1)[:, :K]
+    return (unpack(wq, K) - 8) * s
+
+
+def make(m, K, O, G, dtype, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    W = torch.randn(O, K, generator=g) / math.sqrt(K)
+    x = torch.randn(m, K, generator=g).to(DT[dtype]).cuda()
+    wq, scales = naju.w4_quantize(W.cuda(), G)
+    return x, W, wq, scales
+
+
+def check(x, wq, scales, G, bias=None, residual=None, **kw):
+    K = x.shape[-1]
+    y = naju.w4_linear(x, wq, scales, G, bias=bias, residual=residual, **kw)
+    W = weights(wq, scales, K, G)
+    xd = x.double().cpu().numpy()
+    want, size = xd @ W.T, np.abs(xd) @ np.abs(W).T
+    for t in (bias, residual):
+        if t is not None:
+            want, size = want + t.double().cpu().numpy(), size + t.double().abs().cpu().numpy()
+    allow = 2 * U * (K + 4) * size + 1e-30
+    if x.dtype == torch.bfloat16:
+        allow = allow + 2.0 ** -8 * np.abs(want)
+    err = np.abs(y.double().cpu().numpy() - want)
+    assert y.dtype == x.dtype and np.isfinite(err).all()
+    k = np.unravel_index(np.argmax(err - allow), err.shape)
+    assert err[k] <= allow[k], f"{k}: off by {err[k]:.3e}, allowed {allow[k]:.3e}"
+    return y
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("m", [1, 3, 8, 9, 16, 17, 32, 33, 64, 65, 130, 256])
+def test_rows(m, G, dtype):
+    x, _, wq, scales = make(m, 520, 200, G, dtype, m + G)
+    check(x, wq, scales, G)
+
+
+@pytest.mark.parametrize("K", [1, 7, 31, 32, 33, 127, 128, 129, 1000, 2048, 2500])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_inputs(K, dtype):
+    for m, G in ((1, 128), (11, 32), (40, 64)):
+        x, _, wq, scales = make(m, K, 37, G, dtype, K + m)
+        check(x, wq, scales, G)
+
+
+@pytest.mark.parametrize("O", [1, 15, 16, 17, 127, 129, 1111])
+def test_outputs(O):
+    for m in (1, 20, 70):
+        x, _, wq, scales = make(m, 384, O, 64, "bf16", O + m)
+        check(x, wq, scales, 64)
+
+
+@pytest.mark.parametrize("m,K,O", [(1, 8192, 64), (4, 8192, 300), (64, 8192, 130), (200, 4096, 64)])
+def test_long_rows(m, K, O):
+    """Few rows of weights: the inputs are shared out over a cluster."""
+    for dtype in ("bf16", "f32"):
+        x, _, wq, scales = make(m, K, O, 128, dtype, K + O)
+        y = check(x, wq, scales, 128)
+        assert torch.equal(y, naju.w4_linear(x, wq, scales, 128))  # a fixed order of sums
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_bias_and_residual(dtype):
+    for m in (1, 12, 100):
+        x, _, wq, scales = make(m, 300, 150, 32, dtype, m)
+        bias = torch.randn(150, device="cuda")
+        res = torch.randn(m, 150, device="cuda").to(DT[dtype])
+        check(x, wq, scales, 32, bias=bias)
+        check(x, wq, scales, 32, residual=res)
+        y = check(x, wq, scales, 32, bias=bias, residual=res)
+        assert torch.equal(naju.w4_linear(x, wq, scales, 32, bias=bias, residual=res, y=res), y)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("G", [32, 64, 128])
+def test_quantize(G, dtype):
+    """scale = bf16(max / 7) and q = the nearest, per group, ragged last group."""
+    g = torch.Generator().manual_seed(G)
+    W = (torch.randn(30, 333, generator=g) * torch.randn(30, 1, generator=g).exp()).to(DT[dtype])
+    W[3] = 0
+    W[4, :40] = 0
+    wq, scales = naju.w4_quantize(W.cuda(), G)
+    q = unpack(wq, 333)
+    Wd = W.double().numpy()
+    for i in range(scales.shape[1]):
+        blk = Wd[:, G * i:G * (i + 1)]
+        m = torch.from_numpy(np.abs(blk).max(1)).float()
+        s = (m / 7).bfloat16()
+        assert torch.equal(s, scales[:, i].cpu())
+        sd = s.double().numpy()[:, None]
+        live = sd[:, 0] > 0
+        # fp32 quotients: within half a step of a border either neighbour is right
+        off = np.abs(np.clip(blk[live] / sd[live], -8, 7) - (q[live, G * i:G * (i + 1)] - 8))
+        assert (off <= 0.5 + 8 * U).all()
+        assert (q[~live, G * i:G * (i + 1)] == 8).all()
+
+
+def test_quantize_non_finite():
+    W = torch.randn(4, 256)
+    W[1, 5] = math.inf
+    W[2, 200] = math.nan
+    wq, scales = naju.w4_quantize(W.cuda(), 128)
+    bad = torch.isnan(scales).cpu()
+    assert bad.tolist() == [[False, False], [True, False], [False, True], [False, False]]
+    y = naju.w4_linear(torch.ones(1, 256, device="cuda"), wq, scales, 128)
+    assert torch.isnan(y)[0].tolist() == [False, True, True, False]
+
+
+def test_infinite_and_extreme_inputs():
+    """An infinity meets q = 8 (weight 0) as NaN and others as infinities; the
+    largest fp32 values split without overflow."""
+    x, _, wq, scales = make(2, 128, 16, 128, "f32", 5)
+    W = weights(wq, scales, 128, 128)
+    x.zero_()
+    x[0, 3] = math.inf
+    x[1, 4] = 3.0e38
+    y = naju.w4_linear(x, wq, scales, 128).cpu().numpy()
+    for o in range(16):
+        w = W[o, 3]
+        assert np.isnan(y[0, o]) if w == 0 else y[0, o] == math.copysign(math.inf, w)
+        assert abs(y[1, o] - 3.0e38 * W[o, 4]) <= 4 * U * 3.0e38 * abs(W[o, 4])
+
+
+def test_rows_of_any_leading_shape_and_streams():
+    x, _, wq, scales = make(6, 256, 64, 128, "bf16", 9)
+    y = naju.w4_linear(x, wq, scales)
+    assert torch.equal(naju.w4_linear(x.view(2, 3, 256), wq, scales), y.view(2, 3, 64))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        z = naju.w4_linear(x, wq, scales)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert torch.equal(z, y)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        z = naju.w4_linear(x, wq, scales)
+    x.copy_(torch.randn(6, 256).bfloat16())
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(z, naju.w4_linear(x, wq, scales))
+
+
+def test_neighbours_stay():
+    x, _, wq, scales = make(9, 200, 33, 64, "bf16", 11)
+    buf = torch.full((9 * 33 + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    naju.w4_linear(x, wq, scales, 64, y=buf[:9 * 33].view(9, 33))
+    torch.cuda.synchronize()
+    assert bool((buf[9 * 33:] == 7.0).all())
+
+
+def test_refusals():
+    x, _, wq, scales = make(2, 128, 16, 128, "bf16")
+    with pytest.raises(naju.NajuError):
+        naju.w4_linear(x, wq, scales, 100)
+    with pytest.raises(naju.NajuError):
+        naju.w4_linear(x[:0], wq, scales)
+    with pytest.raises(ValueError):
+        naju.w4_linear(x, wq, scales, 64)
+    with pytest.raises(ValueError):
+        naju.w4_linear(x[:, :100].contiguous(), wq[:, :32].contiguous(), scales)
+    with pytest.raises(TypeError):
+        naju.w4_linear(x.half(), wq, scales)
+    with pytest.raises(ValueError):
+        naju.w4_linear(x, wq, scales, bias=torch.zeros(15, device="cuda"))

@@ -70,3 +70,62 @@ def test_vscan_binding_refuses_cpu_tensors():
         naju.vscan_fwd(h[0], h[0])
     with pytest.raises(ValueError):
         naju.vscan_step(torch.zeros(4, 8), h[0], h[0])
+
+
+def test_state_cache_refusals(L):
+    ok = [FAKE] * 4
+    for f in (L.naju_state_store, L.naju_state_load):
+        assert f(0, 8, 16, 4, *ok, None) == 1
+        assert f(65536, 8, 16, 4, *ok, None) == 1
+        assert f(1, 0, 16, 4, *ok, None) == 1
+        assert f(1, 8, 16, 0, *ok, None) == 1
+        assert f(1, 8, 24, 4, *ok, None) == 2
+        for i in range(4):
+            a = list(ok)
+            a[i] = None
+            assert f(1, 8, 16, 4, *a, None) == 1
+    assert L.naju_state_store(1, 8, 16, 4, MIS, FAKE, FAKE, FAKE, None) == 1
+    assert L.naju_state_load(1, 8, 16, 4, MIS, FAKE, FAKE, FAKE, None) == 1
+
+
+def test_state_cache_binding_refusals():
+    q, s = naju.state_pool(3, 8, 16, "cpu")
+    slots = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        naju.state_load(q, s, slots)
+    with pytest.raises(ValueError):
+        naju.state_load(q[0], s, slots)
+    with pytest.raises(ValueError):
+        naju.state_store(torch.zeros(1, 8, 16), slots[None], q, s)
+
+
+def test_w4_refusals(L):
+    q = lambda *a: L.naju_w4_quantize(*a, None)  # noqa: E731
+    assert q(0, 64, 32, 0, FAKE, FAKE, FAKE) == 1
+    assert q(8, 0, 32, 0, FAKE, FAKE, FAKE) == 1
+    assert q(8, 64, 48, 0, FAKE, FAKE, FAKE) == 2
+    assert q(8, 64, 32, 3, FAKE, FAKE, FAKE) == 2
+    assert q(8, 64, 32, 0, None, FAKE, FAKE) == 1
+    assert q(8, 64, 32, 0, FAKE, MIS, FAKE) == 1
+    f = lambda *a: L.naju_w4_linear(*a, None)  # noqa: E731
+    #        m  in  out  G  dt  x     wq    s     bias  res   y
+    assert f(0, 64, 8, 32, 0, FAKE, FAKE, FAKE, None, None, FAKE) == 1
+    assert f(1 << 21, 64, 8, 32, 0, FAKE, FAKE, FAKE, None, None, FAKE) == 1
+    assert f(1, 64, 0, 32, 0, FAKE, FAKE, FAKE, None, None, FAKE) == 1
+    assert f(1, 64, 8, 16, 0, FAKE, FAKE, FAKE, None, None, FAKE) == 2
+    assert f(1, 64, 8, 32, 2, FAKE, FAKE, FAKE, None, None, FAKE) == 2
+    assert f(1, 64, 8, 32, 0, MIS, FAKE, FAKE, None, None, FAKE) == 1
+    assert f(1, 64, 8, 32, 0, FAKE, MIS, FAKE, None, None, FAKE) == 1
+    assert f(1, 64, 8, 32, 0, FAKE, FAKE, None, None, None, FAKE) == 1
+    assert f(1, 64, 8, 32, 0, FAKE, FAKE, FAKE, None, MIS, FAKE) == 1
+    assert f(1, 64, 8, 32, 0, FAKE, FAKE, FAKE, None, None, None) == 1
+
+
+def test_w4_binding_refusals():
+    with pytest.raises(ValueError):
+        naju.w4_quantize(torch.zeros(8, 64))
+    with pytest.raises(ValueError):
+        naju.w4_quantize(torch.zeros(64))
+    with pytest.raises(ValueError):
+        naju.w4_linear(torch.zeros(1, 64), torch.zeros(8, 64, dtype=torch.uint8),
+                       torch.zeros(8, 1, dtype=torch.bfloat16))
