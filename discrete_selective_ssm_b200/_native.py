@@ -319,56 +319,71 @@ def scan_step_conv(state, conv_state, u, a, b, B, C, conv_w, conv_b=None, z=None
 # ------------------------------------------------------- vector-state scan
 def _arg(t, name: str, shape, dtype, device):
     """Data pointer of an argument that must be a contiguous `dtype` tensor of
-    `shape` on `device` (None passes through)."""
+    `shape` on the CUDA device number `device` (None passes through)."""
     if t is None:
         return None
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on device {device}, got {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _launch(device, stream, call, where: str):
-    """call(raw stream) with `device` current; `stream` defaults to that
-    device's current one."""
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device.index)
-    else:
-        raw = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
-        _check(call(raw), where)
+def _cuda_index(t, name: str) -> int:
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    return i
+
+
+def _launch(fn, device: int, stream, *args):
+    """fn(*args, raw stream) with CUDA device number `device` current; `stream`
+    defaults to that device's current one."""
+    raw = _raw_stream(device) if stream is None else stream.cuda_stream
+    if _get_device() == device:
+        st = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            _check(call(raw), where)
+            st = fn(*args, raw)
+    if st:
+        raise NajuError(st, fn.__name__)
+
+
+def _raw_stream(device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _get_device() -> int:
+    return torch._C._cuda_getDevice()
 
 
 def _vdims(h, out_dtype) -> Dims:
     if h.dim() != 3:
         raise ValueError(f"h must be [batch, seqlen, d_inner], got {tuple(h.shape)}")
-    if not h.is_cuda:
-        raise ValueError("h must be a CUDA tensor")
-    Bt, L, d = h.shape
-    return make_dims(Bt, L, d, 1, _dt(h), out_dtype, 0)
+    dt = _dt(h)
+    return Dims(*h.shape, 1, 0, dt, dt if out_dtype is None else out_dtype, 0)
 
 
 def vscan_workspace(dims: Dims, device) -> torch.Tensor:
     """A workspace of vscan_fwd and vscan_bwd (contents undefined)."""
-    n = int(lib().naju_vscan_workspace_bytes(ctypes.byref(dims)))
+    n = lib().naju_vscan_workspace_bytes(ctypes.byref(dims))
     if n == 0:
         raise NajuError(1, "naju_vscan_workspace_bytes")
-    ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
-    off = (-ws.data_ptr()) % 256
-    return ws[off:off + n]
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    if ws.data_ptr() % 256:  # (an allocator that aligns less than CUDA's)
+        ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
+        off = (-ws.data_ptr()) % 256
+        ws = ws[off:off + n]
+    return ws
 
 
-def _ws_arg(ws, device):
-    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+def _ws_arg(ws, device: int):
+    if ws.dtype is not torch.uint8 or ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on CUDA device {device}")
     return ws.data_ptr()
 
 
@@ -378,20 +393,19 @@ def vscan_fwd(h, a, b=None, *, z=None, x0=None, out_dtype=None, workspace=None, 
     y = x SiLU(z).  b None: coupled gate; z None: no modulation.  Returns
     (y, x_final, workspace); the workspace is what vscan_bwd needs."""
     dims = _vdims(h, out_dtype)
-    dev, dt, act, st = h.device, h.dtype, h.shape, (h.shape[0], h.shape[2])
+    dev, dt, act, f32 = _cuda_index(h, "h"), h.dtype, h.shape, torch.float32
+    st, ot = (act[0], act[2]), _torch_dt(dims.out_dtype)
+    L = _lib or lib()
     if workspace is None:
-        workspace = vscan_workspace(dims, dev)
-    ot = _torch_dt(dims.out_dtype)
+        workspace = vscan_workspace(dims, h.device)
     if y is None:
-        y = torch.empty(act, dtype=ot, device=dev)
+        y = torch.empty_like(h, dtype=ot)
     if x_final is None and want_final:
-        x_final = torch.empty(st, dtype=torch.float32, device=dev)
-    f32, L = torch.float32, lib()
-    args = (ctypes.byref(dims), _arg(h, "h", act, dt, dev), _arg(a, "a", act, dt, dev),
-            _arg(b, "b", act, dt, dev), _arg(z, "z", act, dt, dev), _arg(x0, "x0", st, f32, dev),
-            _arg(y, "y", act, ot, dev), _arg(x_final, "x_final", st, f32, dev),
-            _ws_arg(workspace, dev), workspace.numel())
-    _launch(dev, stream, lambda s: L.naju_vscan_fwd(*args, s), "naju_vscan_fwd")
+        x_final = torch.empty(st, dtype=f32, device=h.device)
+    _launch(L.naju_vscan_fwd, dev, stream, ctypes.byref(dims), _arg(h, "h", act, dt, dev),
+            _arg(a, "a", act, dt, dev), _arg(b, "b", act, dt, dev), _arg(z, "z", act, dt, dev),
+            _arg(x0, "x0", st, f32, dev), _arg(y, "y", act, ot, dev),
+            _arg(x_final, "x_final", st, f32, dev), _ws_arg(workspace, dev), workspace.numel())
     return y, x_final, workspace
 
 
@@ -401,37 +415,37 @@ def vscan_bwd(dy, h, a, b, workspace, *, z=None, dx_final=None, out_dtype=None, 
     checkpoints.  Returns a dict: dh, da, db (None without b), dz (None
     without z), dx0 (None unless wanted)."""
     dims = _vdims(h, out_dtype)
-    dev, dt, act, st = h.device, h.dtype, h.shape, (h.shape[0], h.shape[2])
-    ot, f32 = _torch_dt(dims.out_dtype), torch.float32
+    dev, dt, act, f32 = _cuda_index(h, "h"), h.dtype, h.shape, torch.float32
+    st, ot = (act[0], act[2]), _torch_dt(dims.out_dtype)
+    L = _lib or lib()
     if grads is None:
-        new = lambda want=True: torch.empty(act, dtype=ot, device=dev) if want else None  # noqa: E731
-        grads = {"dh": new(), "da": new(), "db": new(b is not None), "dz": new(z is not None),
-                 "dx0": torch.empty(st, dtype=f32, device=dev) if want_dx0 else None}
+        grads = {"dh": torch.empty_like(h, dtype=ot), "da": torch.empty_like(h, dtype=ot),
+                 "db": None if b is None else torch.empty_like(h, dtype=ot),
+                 "dz": None if z is None else torch.empty_like(h, dtype=ot),
+                 "dx0": torch.empty(st, dtype=f32, device=h.device) if want_dx0 else None}
     g = grads
-    L = lib()
-    args = (ctypes.byref(dims), _arg(h, "h", act, dt, dev), _arg(a, "a", act, dt, dev),
-            _arg(b, "b", act, dt, dev), _arg(z, "z", act, dt, dev),
+    _launch(L.naju_vscan_bwd, dev, stream, ctypes.byref(dims), _arg(h, "h", act, dt, dev),
+            _arg(a, "a", act, dt, dev), _arg(b, "b", act, dt, dev), _arg(z, "z", act, dt, dev),
             _arg(dy, "dy", act, dt, dev), _arg(dx_final, "dx_final", st, f32, dev),
             _arg(g["dh"], "dh", act, ot, dev), _arg(g["da"], "da", act, ot, dev),
             _arg(g.get("db"), "db", act, ot, dev), _arg(g.get("dz"), "dz", act, ot, dev),
             _arg(g.get("dx0"), "dx0", st, f32, dev), _ws_arg(workspace, dev), workspace.numel())
-    _launch(dev, stream, lambda s: L.naju_vscan_bwd(*args, s), "naju_vscan_bwd")
     return g
 
 
 def vscan_step(state, h, a, b=None, z=None, y=None, stream=None):
     """One decode step of the vector-state scan: h, a, b, z [batch, d_inner];
     `state` [batch, d_inner] fp32 is updated in place.  Returns y."""
-    if h.dim() != 2:
-        raise ValueError(f"h must be [batch, d_inner], got {tuple(h.shape)}")
-    dev, dt, sh = h.device, h.dtype, h.shape
+    sh = h.shape
+    if len(sh) != 2:
+        raise ValueError(f"h must be [batch, d_inner], got {tuple(sh)}")
+    dev, dt, code = _cuda_index(h, "h"), h.dtype, _dt(h)
+    L = _lib or lib()
     if y is None:
         y = torch.empty_like(h)
-    L = lib()
-    args = (sh[0], sh[1], _dt(h), _arg(h, "h", sh, dt, dev), _arg(a, "a", sh, dt, dev),
-            _arg(b, "b", sh, dt, dev), _arg(z, "z", sh, dt, dev),
+    _launch(L.naju_vscan_step, dev, stream, sh[0], sh[1], code, _arg(h, "h", sh, dt, dev),
+            _arg(a, "a", sh, dt, dev), _arg(b, "b", sh, dt, dev), _arg(z, "z", sh, dt, dev),
             _arg(state, "state", sh, torch.float32, dev), _arg(y, "y", sh, dt, dev))
-    _launch(dev, stream, lambda s: L.naju_vscan_step(*args, s), "naju_vscan_step")
     return y
 
 
@@ -449,13 +463,12 @@ def w4_quantize(W, group=128, stream=None):
     if W.dim() != 2:
         raise ValueError(f"W must be [n_out, n_in], got {tuple(W.shape)}")
     _w4_group(group)
-    dev, (O, K) = W.device, W.shape
-    w = _arg(W, "W", W.shape, W.dtype, dev)
-    wq = torch.empty((O, -(-K // 128) * 64), dtype=torch.uint8, device=dev)
-    scales = torch.empty((O, -(-K // group)), dtype=torch.bfloat16, device=dev)
-    args = (O, K, group, _dt(W), w, wq.data_ptr(), scales.data_ptr())
-    L = lib()
-    _launch(dev, stream, lambda s: L.naju_w4_quantize(*args, s), "naju_w4_quantize")
+    dev, (O, K), code = _cuda_index(W, "W"), W.shape, _dt(W)
+    L = _lib or lib()
+    wq = torch.empty((O, -(-K // 128) * 64), dtype=torch.uint8, device=W.device)
+    scales = torch.empty((O, -(-K // group)), dtype=torch.bfloat16, device=W.device)
+    _launch(L.naju_w4_quantize, dev, stream, O, K, group, code,
+            _arg(W, "W", W.shape, W.dtype, dev), wq.data_ptr(), scales.data_ptr())
     return wq, scales
 
 
@@ -464,19 +477,17 @@ def w4_linear(x, wq, scales, group=128, bias=None, residual=None, y=None, stream
     x [..., n_in] (its leading dimensions are rows), bias [n_out] fp32, residual
     and y [..., n_out] in x's dtype."""
     _w4_group(group)
-    dev, dt, K = x.device, x.dtype, x.shape[-1]
-    O = wq.shape[0]
-    out = x.shape[:-1] + (O,)
+    sh, O = x.shape, wq.shape[0]
+    dev, dt, K, code = _cuda_index(x, "x"), x.dtype, sh[-1], _dt(x)
+    out = (*sh[:-1], O)
+    L = _lib or lib()
     if y is None:
-        y = torch.empty(out, dtype=dt, device=dev)
-    m = x.numel() // K if K else 0
-    args = (m, K, O, group, _dt(x), _arg(x, "x", x.shape, dt, dev),
-            _arg(wq, "wq", (O, -(-K // 128) * 64), torch.uint8, dev),
+        y = torch.empty(out, dtype=dt, device=x.device)
+    _launch(L.naju_w4_linear, dev, stream, x.numel() // K if K else 0, K, O, group, code,
+            _arg(x, "x", sh, dt, dev), _arg(wq, "wq", (O, -(-K // 128) * 64), torch.uint8, dev),
             _arg(scales, "scales", (O, -(-K // group)), torch.bfloat16, dev),
             _arg(bias, "bias", (O,), torch.float32, dev),
             _arg(residual, "residual", out, dt, dev), _arg(y, "y", out, dt, dev))
-    L = lib()
-    _launch(dev, stream, lambda s: L.naju_w4_linear(*args, s), "naju_w4_linear")
     return y
 
 
@@ -489,15 +500,16 @@ def state_pool(n_slots: int, d_inner: int, d_state: int, device):
 
 
 def _cache_args(pool_q, pool_scale, slots):
-    if pool_q.dim() != 3:
-        raise ValueError(f"pool_q must be [n_slots, d_inner, d_state], got {tuple(pool_q.shape)}")
+    sh = pool_q.shape
+    if len(sh) != 3:
+        raise ValueError(f"pool_q must be [n_slots, d_inner, d_state], got {tuple(sh)}")
     if slots.dim() != 1:
         raise ValueError(f"slots must be [n], got {tuple(slots.shape)}")
-    (S, d, N), dev = pool_q.shape, pool_q.device
+    dev = _cuda_index(pool_q, "pool_q")
     n = slots.shape[0]
-    return ((n, d, N, S), dev, _arg(pool_q, "pool_q", pool_q.shape, torch.int8, dev),
-            _arg(pool_scale, "pool_scale", pool_q.shape[:2], torch.float32, dev),
-            _arg(slots, "slots", slots.shape, torch.int32, dev))
+    return (dev, (n, sh[1], sh[2], sh[0]), _arg(pool_q, "pool_q", sh, torch.int8, dev),
+            _arg(pool_scale, "pool_scale", sh[:2], torch.float32, dev),
+            _arg(slots, "slots", (n,), torch.int32, dev))
 
 
 def state_store(state, slots, pool_q, pool_scale, stream=None):
@@ -505,23 +517,19 @@ def state_store(state, slots, pool_q, pool_scale, stream=None):
     into slot slots[i] (int32) of the pool, 8 bits a value with one scale per
     row.  Slots outside the pool store nothing; of places that name the same
     slot the last is stored."""
-    sizes, dev, q, sc, sl = _cache_args(pool_q, pool_scale, slots)
-    st = _arg(state, "state", sizes[:3], torch.float32, dev)
-    L = lib()
-    _launch(dev, stream, lambda s: L.naju_state_store(*sizes, st, sl, q, sc, s),
-            "naju_state_store")
+    dev, sizes, q, sc, sl = _cache_args(pool_q, pool_scale, slots)
+    _launch((_lib or lib()).naju_state_store, dev, stream, *sizes,
+            _arg(state, "state", sizes[:3], torch.float32, dev), sl, q, sc)
 
 
 def state_load(pool_q, pool_scale, slots, state=None, stream=None):
     """Resumes parked states: slot slots[i] into batch place i.  Slots outside
     the pool give a zero state.  Returns state [n, d_inner, d_state] fp32."""
-    sizes, dev, q, sc, sl = _cache_args(pool_q, pool_scale, slots)
+    dev, sizes, q, sc, sl = _cache_args(pool_q, pool_scale, slots)
     if state is None:
-        state = torch.empty(sizes[:3], dtype=torch.float32, device=dev)
-    st = _arg(state, "state", sizes[:3], torch.float32, dev)
-    L = lib()
-    _launch(dev, stream, lambda s: L.naju_state_load(*sizes, q, sc, sl, st, s),
-            "naju_state_load")
+        state = torch.empty(sizes[:3], dtype=torch.float32, device=pool_q.device)
+    _launch((_lib or lib()).naju_state_load, dev, stream, *sizes, q, sc, sl,
+            _arg(state, "state", sizes[:3], torch.float32, dev))
     return state
 
 

@@ -4,11 +4,28 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "naju.h"
 
 namespace naju {
 
 struct WsHeader;
+
+// Sets a kernel's dynamic shared memory limit (and lets clusters pass eight
+// blocks) once per device; `ready` is the kernel's own record of devices.
+inline cudaError_t smem_once(const void* kern, int smem, std::atomic<uint64_t>& ready) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ULL << dev : 0;
+    if (bit && (ready.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && bit) ready.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // Host-side validation of the dims shared by every sequence entry point:
 // NAJU_OK, NAJU_ERR_INVALID_ARG (sizes out of range) or NAJU_ERR_UNSUPPORTED.

@@ -230,7 +230,9 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
 template <typename Tin, typename Tout, bool HASB, bool HASZ, bool TMA, bool VEC>
 static cudaError_t fwd_k(const VscanParams& p, const VscanMaps& maps, cudaStream_t st) {
     const int smem = TMA ? (2 + HASB + HASZ) * kVTokF * 128 : 0;
-    return vscan_launch(vscan_fwd_kernel<Tin, Tout, HASB, HASZ, TMA, VEC>, p, maps, smem, st);
+    static std::atomic<uint64_t> ready{0};
+    return vscan_launch(vscan_fwd_kernel<Tin, Tout, HASB, HASZ, TMA, VEC>, p, maps, smem, ready,
+                        st);
 }
 
 template <typename Tin, typename Tout, bool TMA, bool VEC>

@@ -282,10 +282,9 @@ template <int CP> struct VExchange {
 // Launches a kernel over p.units clusters of p.cluster blocks.
 template <typename Maps>
 inline cudaError_t vscan_launch(void (*kern)(VscanParams, Maps), const VscanParams& p,
-                                const Maps& maps, int smem, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess && p.cluster > 8)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+                                const Maps& maps, int smem, std::atomic<uint64_t>& ready,
+                                cudaStream_t st) {
+    const cudaError_t e = smem_once(reinterpret_cast<const void*>(kern), smem, ready);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p.units * p.cluster));

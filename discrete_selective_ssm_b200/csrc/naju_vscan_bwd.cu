@@ -274,7 +274,9 @@ vscan_bwd_kernel(const __grid_constant__ VscanParams p,
 template <typename Tin, typename Tout, bool HASB, bool HASZ, bool TMA, bool VEC>
 static cudaError_t bwd_k(const VscanParams& p, const VscanBwdMaps& maps, cudaStream_t st) {
     const int smem = TMA ? (3 + HASB + HASZ) * kVTokB * 128 : 0;
-    return vscan_launch(vscan_bwd_kernel<Tin, Tout, HASB, HASZ, TMA, VEC>, p, maps, smem, st);
+    static std::atomic<uint64_t> ready{0};
+    return vscan_launch(vscan_bwd_kernel<Tin, Tout, HASB, HASZ, TMA, VEC>, p, maps, smem, ready,
+                        st);
 }
 
 template <typename Tin, typename Tout, bool TMA, bool VEC>

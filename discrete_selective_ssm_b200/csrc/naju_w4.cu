@@ -18,6 +18,8 @@
 // lanes' j-th words are one run of 32 inputs (so that groups of 32 work).
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "naju_common.cuh"
 #include "naju_kernels.h"
 
@@ -129,18 +131,20 @@ struct W4Params {
     int split;                       // blocks of a cluster, each with a share of the inputs
 };
 
-// WR warps along the rows of W (16 each), WK along the inputs; NT tiles of 8
-// rows of x.  A chunk is BPW blocks of 128 inputs for each of the WK warps.
+// General form.  WR warps along the rows of W (16 each), WK along the inputs;
+// NT tiles of 8 rows of x.  A chunk is BPW blocks of 128 inputs for each of the
+// WK warps; the next chunk's x comes into the other half of the stage and its
+// weights into registers while this one is computed.
 template <typename T, int WR, int WK, int NT, int G>
 __global__ void __launch_bounds__(256) w4_linear_kernel(const W4Params p) {
     constexpr int SP = sizeof(T) == 4 ? 3 : 1;   // bf16 parts of an x value
-    constexpr int BPW = 2, KC = BPW * WK;        // blocks per warp and chunk, per chunk
+    constexpr int BPW = SP == 1 ? 2 : 1, KC = BPW * WK;  // blocks per warp and chunk, per chunk
     constexpr int GPB = 128 / G;                 // groups per block
     constexpr int ROWS = 16 * WR, COLS = 8 * NT;
     static_assert(WR * WK == 8, "eight warps");
-    // x as operand fragments: [part][block][j][tile][n][c] of 16 bytes (8 inputs)
+    // x as operand fragments, twice: [part][block][j][tile][n][c] of 16 bytes (8 inputs)
     extern __shared__ __align__(16) unsigned char smem[];
-    uint4* xs = reinterpret_cast<uint4*>(smem);
+    uint4* xs0 = reinterpret_cast<uint4*>(smem);
     float* red = reinterpret_cast<float*>(smem);  // [WK][COLS][ROWS] after the last chunk
     constexpr int PART = KC * 4 * NT * 32;        // 16-byte units of one part
     namespace cg = cooperative_groups;
@@ -163,8 +167,8 @@ __global__ void __launch_bounds__(256) w4_linear_kernel(const W4Params p) {
             const int64_t b = ch * KC + i * WK + wk;
             wa[i] = wb[i] = make_uint4(0, 0, 0, 0);
             if (b < p.nb) {
-                if (ra < p.n_out) wa[i] = __ldcs(p.wq + (ra * p.nb + b) * 4 + c);
-                if (rb < p.n_out) wb[i] = __ldcs(p.wq + (rb * p.nb + b) * 4 + c);
+                if (ra < p.n_out) wa[i] = __ldg(p.wq + (ra * p.nb + b) * 4 + c);
+                if (rb < p.n_out) wb[i] = __ldg(p.wq + (rb * p.nb + b) * 4 + c);
             }
 #pragma unroll
             for (int g = 0; g < GPB; ++g) {
@@ -177,7 +181,7 @@ __global__ void __launch_bounds__(256) w4_linear_kernel(const W4Params p) {
     };
     const T* x = static_cast<const T*>(p.x);
     const bool xvec = p.n_in % (16 / sizeof(T)) == 0;  // rows start on 16 bytes
-    const auto stage_x = [&](int64_t ch) {
+    const auto stage_x = [&](int64_t ch, uint4* xs) {
         for (int e = tid; e < KC * 16 * COLS; e += 256) {
             const int unit = e % (KC * 16), n = e / (KC * 16);  // 8 inputs of one row of x
             const int64_t k = ch * KC * 128 + unit * 8, row = col0 + n;
@@ -185,19 +189,18 @@ __global__ void __launch_bounds__(256) w4_linear_kernel(const W4Params p) {
             const int at = ((b * 4 + j) * NT + n / 8) * 32 + n % 8 * 4 + cc;
             const bool in = row < p.m;
             if constexpr (SP == 1) {
-                uint4 v = make_uint4(0, 0, 0, 0);
                 const __nv_bfloat16* src = x + row * p.n_in + k;
-                if (in && xvec) {
-                    if (k < p.n_in) v = __ldg(reinterpret_cast<const uint4*>(src));
-                } else if (in) {
+                if (xvec) {
+                    const bool ok = in && k < p.n_in;
+                    cp_async16(xs + at, ok ? src : x, ok ? 16 : 0);
+                } else {
                     uint32_t h[8];
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        h[q] = k + q < p.n_in ? __bfloat16_as_ushort(src[q]) : 0u;
-                    v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
-                                   h[6] | h[7] << 16);
+                        h[q] = in && k + q < p.n_in ? __bfloat16_as_ushort(src[q]) : 0u;
+                    xs[at] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
+                                        h[6] | h[7] << 16);
                 }
-                xs[at] = v;
             } else {
                 float f[8];
                 const float* src = x + row * p.n_in + k;
@@ -227,10 +230,15 @@ __global__ void __launch_bounds__(256) w4_linear_kernel(const W4Params p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
 
-    if (ch0 < ch1) load_w(ch0);
+    if (ch0 < ch1) {
+        load_w(ch0);
+        stage_x(ch0, xs0);
+        cp_async_commit();
+    }
     for (int64_t ch = ch0; ch < ch1; ++ch) {
-        stage_x(ch);
-        __syncthreads();
+        const uint4* xs = xs0 + ((ch - ch0) & 1) * SP * PART;
+        cp_async_wait<0>();
+        __syncthreads();  // this chunk's x is there, the other half is read
         uint4 ca[BPW], cb[BPW];
         float fa[BPW][GPB], fb[BPW][GPB];
 #pragma unroll
@@ -243,7 +251,11 @@ __global__ void __launch_bounds__(256) w4_linear_kernel(const W4Params p) {
                 fb[i][g] = __bfloat162float(sb[i][g]);
             }
         }
-        if (ch + 1 < ch1) load_w(ch + 1);
+        if (ch + 1 < ch1) {
+            load_w(ch + 1);
+            stage_x(ch + 1, xs0 + ((ch + 1 - ch0) & 1) * SP * PART);
+            cp_async_commit();
+        }
 #pragma unroll
         for (int i = 0; i < BPW; ++i) {
             const uint32_t* ua = reinterpret_cast<const uint32_t*>(&ca[i]);
@@ -285,8 +297,8 @@ __global__ void __launch_bounds__(256) w4_linear_kernel(const W4Params p) {
                 }
             }
         }
-        __syncthreads();
     }
+    __syncthreads();
 
     // sums over the WK warps, then over the cluster's blocks, in fixed order
 #pragma unroll
@@ -320,20 +332,132 @@ __global__ void __launch_bounds__(256) w4_linear_kernel(const W4Params p) {
     if (p.split > 1) cl.sync();  // no block leaves while another reads from it
 }
 
-template <typename T, int WR, int WK, int NT, int G>
-static cudaError_t w4_run(W4Params p, int sms, cudaStream_t st) {
-    constexpr int SP = sizeof(T) == 4 ? 3 : 1, KC = 2 * WK;
-    constexpr int xbytes = SP * KC * 4 * NT * 32 * 16, rbytes = WK * 8 * NT * 16 * WR * 4;
-    constexpr int smem = xbytes > rbytes ? xbytes : rbytes;
-    const int64_t rt = (p.n_out + 16 * WR - 1) / (16 * WR), ct = (p.m + 8 * NT - 1) / (8 * NT);
-    const int64_t nch = (p.nb + KC - 1) / KC;
-    p.split = 1;
-    while (p.split < 8 && 2 * p.split <= nch && rt * ct * p.split < 3LL * sms) p.split *= 2;
-    auto kern = w4_linear_kernel<T, WR, WK, NT, G>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// Up to eight rows of bf16 x that start on 16 bytes (the decode of a few
+// sessions, where the time is that of reading the weights): no stage and no
+// barrier before the sum.  Eight warps share 16 rows of W, each takes every
+// eighth block of the inputs (of this block's share), the x of its fragments
+// straight from global memory (L1 holds it: all rows of W use the same), and
+// has the weights of its next UB blocks in flight.
+template <int G>
+__global__ void __launch_bounds__(256, 2) w4_rows_kernel(const W4Params p) {
+    constexpr int GPB = 128 / G, UB = 4;
+    __shared__ float red[8][8][16];  // [warp][row of x][row of W]
+    namespace cg = cooperative_groups;
+    typedef __nv_bfloat16 bf;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned rank = blockIdx.x % p.split;
+    const int64_t row0 = (int64_t)(blockIdx.x / p.split) * 16;
+    const int r = lane >> 2, c = lane & 3;
+    const bool oka = row0 + r < p.n_out, okb = row0 + r + 8 < p.n_out;
+    const int nb = (int)p.nb, step = 8 * p.split;
+    const uint4* wa = p.wq + (oka ? (row0 + r) * p.nb * 4 : 0) + c;
+    const uint4* wb = p.wq + (okb ? (row0 + r + 8) * p.nb * 4 : 0) + c;
+    const bf* sa = p.scales + (oka ? (row0 + r) * p.ng : 0);
+    const bf* sb = p.scales + (okb ? (row0 + r + 8) * p.ng : 0);
+    const bool okx = r < p.m;
+    const bf* x = static_cast<const bf*>(p.x) + (okx ? r * p.n_in : 0) + 8 * c;
+
+    uint4 qa[UB], qb[UB];
+    bf fa[UB][GPB], fb[UB][GPB];
+    const auto load = [&](int b0) {
+#pragma unroll
+        for (int i = 0; i < UB; ++i) {
+            const int b = b0 + i * step;
+            qa[i] = qb[i] = make_uint4(0, 0, 0, 0);
+            if (b < nb) {
+                if (oka) qa[i] = __ldg(wa + (int64_t)b * 4);
+                if (okb) qb[i] = __ldg(wb + (int64_t)b * 4);
+            }
+#pragma unroll
+            for (int g = 0; g < GPB; ++g) {
+                const int gi = b * GPB + g;
+                const bool ok = b < nb && gi < p.ng;
+                fa[i][g] = ok && oka ? sa[gi] : bf(0.f);
+                fb[i][g] = ok && okb ? sb[gi] : bf(0.f);
+            }
+        }
+    };
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    int b0 = rank * 8 + warp;
+    load(b0);
+    for (; b0 < nb; b0 += UB * step) {
+        uint4 ca[UB], cb[UB];
+        float ga[UB][GPB], gb[UB][GPB];
+#pragma unroll
+        for (int i = 0; i < UB; ++i) {
+            ca[i] = qa[i];
+            cb[i] = qb[i];
+#pragma unroll
+            for (int g = 0; g < GPB; ++g) {
+                ga[i][g] = __bfloat162float(fa[i][g]);
+                gb[i][g] = __bfloat162float(fb[i][g]);
+            }
+        }
+        load(b0 + UB * step);
+#pragma unroll
+        for (int i = 0; i < UB; ++i) {
+            const int b = b0 + i * step;
+            if (b >= nb) break;
+            uint4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = b * 128 + 32 * j;
+                v[j] = make_uint4(0, 0, 0, 0);
+                if (okx && k + 8 * c < p.n_in) v[j] = __ldg(reinterpret_cast<const uint4*>(x + k));
+            }
+            const uint32_t* ua = reinterpret_cast<const uint32_t*>(&ca[i]);
+            const uint32_t* ub = reinterpret_cast<const uint32_t*>(&cb[i]);
+            float part[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j % (4 / GPB) == 0) part[0] = part[1] = part[2] = part[3] = 0.f;
+                mma_bf16(part, unpack_pair(ua[j], 0), unpack_pair(ub[j], 0), unpack_pair(ua[j], 1),
+                         unpack_pair(ub[j], 1), v[j].x, v[j].y);
+                mma_bf16(part, unpack_pair(ua[j], 2), unpack_pair(ub[j], 2), unpack_pair(ua[j], 3),
+                         unpack_pair(ub[j], 3), v[j].z, v[j].w);
+                if ((j + 1) % (4 / GPB) == 0) {
+                    const int g = j / (4 / GPB);
+                    acc[0] = fmaf(ga[i][g], part[0], acc[0]);
+                    acc[1] = fmaf(ga[i][g], part[1], acc[1]);
+                    acc[2] = fmaf(gb[i][g], part[2], acc[2]);
+                    acc[3] = fmaf(gb[i][g], part[3], acc[3]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) red[warp][c * 2 + (e & 1)][r + (e >> 1) * 8] = acc[e];
+    cg::cluster_group cl = cg::this_cluster();
+    if (p.split > 1)
+        cl.sync();
+    else
+        __syncthreads();
+    for (int e = rank * 256 + tid; e < 128; e += 256 * p.split) {
+        const int row = e % 16, col = e / 16;
+        const int64_t o = row0 + row;
+        if (o >= p.n_out || col >= p.m) continue;
+        float v = 0.f;
+        for (int s = 0; s < p.split; ++s) {
+            const float* from = p.split > 1 ? cl.map_shared_rank(&red[0][0][0], s) : &red[0][0][0];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v += from[(k * 8 + col) * 16 + row];
+        }
+        v *= 1024.f;
+        if (p.bias) v += p.bias[o];
+        if (p.residual) v += to_f(static_cast<const bf*>(p.residual)[col * p.n_out + o]);
+        static_cast<bf*>(p.y)[col * p.n_out + o] = from_f<bf>(v);
+    }
+    if (p.split > 1) cl.sync();
+}
+
+// Launches clusters of p.split blocks.  `ready`: the devices on which this
+// kernel's attributes are set.
+static cudaError_t w4_launch(void (*kern)(const W4Params), const W4Params& p, dim3 grid, int smem,
+                             std::atomic<uint64_t>& ready, cudaStream_t st) {
+    cudaError_t e = smem_once(reinterpret_cast<const void*>(kern), smem, ready);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(rt * p.split), (unsigned)ct);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -346,8 +470,36 @@ static cudaError_t w4_run(W4Params p, int sms, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+template <int G>
+static cudaError_t w4_rows(W4Params p, int sms, cudaStream_t st) {
+    static std::atomic<uint64_t> ready{0};
+    const int64_t rt = (p.n_out + 15) / 16;
+    // share the inputs out while the blocks do not fill two per SM and every
+    // warp keeps a block of them
+    p.split = 1;
+    while (p.split < 8 && 16 * p.split <= p.nb && rt * p.split * 2 <= 4LL * sms) p.split *= 2;
+    return w4_launch(w4_rows_kernel<G>, p, dim3((unsigned)(rt * p.split)), 0, ready, st);
+}
+
+template <typename T, int WR, int WK, int NT, int G>
+static cudaError_t w4_run(W4Params p, int sms, cudaStream_t st) {
+    constexpr int SP = sizeof(T) == 4 ? 3 : 1, KC = (SP == 1 ? 2 : 1) * WK;
+    constexpr int xbytes = 2 * SP * KC * 4 * NT * 32 * 16, rbytes = WK * 8 * NT * 16 * WR * 4;
+    constexpr int smem = xbytes > rbytes ? xbytes : rbytes;
+    const int64_t rt = (p.n_out + 16 * WR - 1) / (16 * WR), ct = (p.m + 8 * NT - 1) / (8 * NT);
+    const int64_t nch = (p.nb + KC - 1) / KC;
+    p.split = 1;
+    while (p.split < 8 && 2 * p.split <= nch && rt * ct * p.split < 3LL * sms) p.split *= 2;
+    static std::atomic<uint64_t> ready{0};
+    return w4_launch(w4_linear_kernel<T, WR, WK, NT, G>, p,
+                     dim3((unsigned)(rt * p.split), (unsigned)ct), smem, ready, st);
+}
+
 template <typename T, int G>
 static cudaError_t w4_pick(const W4Params& p, int sms, cudaStream_t st) {
+    if constexpr (sizeof(T) == 2) {
+        if (p.m <= 8 && p.n_in % 8 == 0) return w4_rows<G>(p, sms, st);
+    }
     if (p.m <= 8) return w4_run<T, 1, 8, 1, G>(p, sms, st);
     if (p.m <= 16) return w4_run<T, 2, 4, 2, G>(p, sms, st);
     if (p.m <= 32) return w4_run<T, 4, 2, 4, G>(p, sms, st);
