@@ -18,10 +18,9 @@
 // lanes' j-th words are one run of 32 inputs (so that groups of 32 work).
 #include <cooperative_groups.h>
 
-#include <atomic>
-
 #include "naju_common.cuh"
 #include "naju_kernels.h"
+#include "naju_w4.cuh"
 
 namespace naju {
 
@@ -92,18 +91,6 @@ __device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Nibbles i and i + 4 of a word (inputs 2 i, 2 i + 1) as two bf16 of
-// (q - 8) / 1024: or-ing q into the bits of 128 gives 128 + q, exactly.  The
-// factor keeps a group's sum (at most 128 * 8 values of x) in range for every
-// finite x; the sums are multiplied by 1024 once, at the end.
-__device__ __forceinline__ uint32_t unpack_pair(uint32_t w, int i) {
-    uint32_t t = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 r =
-        __hfma2(*reinterpret_cast<__nv_bfloat162*>(&t), __float2bfloat162_rn(1.f / 1024.f),
-                __float2bfloat162_rn(-136.f / 1024.f));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 // fp32 as three bf16 that add up to it (each takes the leading 8 bits of what
 // is left, cut off, so nothing overflows); an infinity or a NaN in the first.
 __device__ __forceinline__ void split3(float x, uint32_t& h, uint32_t& m, uint32_t& l) {
@@ -119,17 +106,6 @@ __device__ __forceinline__ void split3(float x, uint32_t& h, uint32_t& m, uint32
     m = mb >> 16;
     l = __float_as_uint(r - __uint_as_float(mb)) >> 16;
 }
-
-struct W4Params {
-    const void* x;
-    const uint4* wq;
-    const __nv_bfloat16* scales;
-    const float* bias;
-    const void* residual;
-    void* y;
-    int64_t m, n_in, n_out, nb, ng;  // nb: 128-input blocks of a row, ng: groups of a row
-    int split;                       // blocks of a cluster, each with a share of the inputs
-};
 
 // General form.  WR warps along the rows of W (16 each), WK along the inputs;
 // NT tiles of 8 rows of x.  A chunk is BPW blocks of 128 inputs for each of the
@@ -224,6 +200,7 @@ __global__ void __launch_bounds__(256) w4_linear_kernel(const W4Params p) {
         }
     };
 
+    const PairBits bits;
     float acc[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -273,8 +250,8 @@ __global__ void __launch_bounds__(256) w4_linear_kernel(const W4Params p) {
                 uint32_t pa[4], pb[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    pa[q] = unpack_pair(ua[j], q);
-                    pb[q] = unpack_pair(ub[j], q);
+                    pa[q] = unpack_pair(ua[j], q, bits);
+                    pb[q] = unpack_pair(ub[j], q, bits);
                 }
 #pragma unroll
                 for (int s = 0; s < SP; ++s) {
@@ -332,153 +309,211 @@ __global__ void __launch_bounds__(256) w4_linear_kernel(const W4Params p) {
     if (p.split > 1) cl.sync();  // no block leaves while another reads from it
 }
 
-// Up to eight rows of bf16 x that start on 16 bytes (the decode of a few
-// sessions, where the time is that of reading the weights): no stage and no
-// barrier before the sum.  Eight warps share 16 rows of W, each takes every
-// eighth block of the inputs (of this block's share), the x of its fragments
-// straight from global memory (L1 holds it: all rows of W use the same), and
-// has the weights of its next UB blocks in flight.
-template <int G>
-__global__ void __launch_bounds__(256, 2) w4_rows_kernel(const W4Params p) {
-    constexpr int GPB = 128 / G, UB = 4;
-    __shared__ float red[8][8][16];  // [warp][row of x][row of W]
-    namespace cg = cooperative_groups;
-    typedef __nv_bfloat16 bf;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const unsigned rank = blockIdx.x % p.split;
-    const int64_t row0 = (int64_t)(blockIdx.x / p.split) * 16;
-    const int r = lane >> 2, c = lane & 3;
-    const bool oka = row0 + r < p.n_out, okb = row0 + r + 8 < p.n_out;
-    const int nb = (int)p.nb, step = 8 * p.split;
-    const uint4* wa = p.wq + (oka ? (row0 + r) * p.nb * 4 : 0) + c;
-    const uint4* wb = p.wq + (okb ? (row0 + r + 8) * p.nb * 4 : 0) + c;
-    const bf* sa = p.scales + (oka ? (row0 + r) * p.ng : 0);
-    const bf* sb = p.scales + (okb ? (row0 + r + 8) * p.ng : 0);
-    const bool okx = r < p.m;
-    const bf* x = static_cast<const bf*>(p.x) + (okx ? r * p.n_in : 0) + 8 * c;
+// One or two rows of x (the decode of one or two sessions: the time is that of
+// reading the weights), on the CUDA cores.  A warp takes kR rows of W (a tile)
+// and 1024 inputs of each (a slice) at a time, 16 bytes a lane, so its loads
+// are whole lines and a value of x serves kR weights.  A nibble becomes a float
+// without a conversion: or-ed into the bits of 2^23 at nibble place i (0 to 3)
+// it reads 2^23 + 16^i q, and a packed addition of two such leaves
+// 16^i (q - 8), exactly; the 16^-i (and the 1 / 1024 of unpack_pair) is in the x
+// that is staged.  A word's eight products are summed unscaled and enter the
+// row's sum with its group's scale.
+// Blocks stay resident: x is staged once, and a warp goes on from tile to tile
+// while its next kDepth slices of W are on their way into its own part of
+// shared memory (cp.async, each lane its own 16 bytes: no barrier).
+constexpr int kR = 4;           // rows of W per tile
+constexpr int kRowsSlices = 32; // most slices of x (all its rows) in shared memory
+constexpr int kDepth = 4;
 
-    uint4 qa[UB], qb[UB];
-    bf fa[UB][GPB], fb[UB][GPB];
-    const auto load = [&](int b0) {
+// Nibbles i of the two halves of a word (inputs 2 i, 2 i + 1): 16^i (q - 8).
+__device__ __forceinline__ float2 nibble_pair(uint32_t lo, uint32_t hi, int i, uint32_t magic) {
+    const float c = -(8388608.f + (float)(8 << (4 * i)));
+    return __fadd2_rn(make_float2(__uint_as_float(and_or(lo, 0xfu << (4 * i), magic)),
+                                  __uint_as_float(and_or(hi, 0xfu << (4 * i), magic))),
+                      make_float2(c, c));
+}
+
+template <typename T, int G, int MR>
+__global__ void __launch_bounds__(256, 2) w4_rows_kernel(const W4Params p) {
+    constexpr int GPB = 128 / G;
+    extern __shared__ __align__(16) unsigned char smem[];
+    uint4* ring = reinterpret_cast<uint4*>(smem);  // [warp][kDepth][kR][lane]
+    float4* xs = reinterpret_cast<float4*>(ring + 8 * kDepth * kR * 32);
+    // xs: [row of x][slice][j][half][lane]
+    __shared__ float red[2][8][kR][MR];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int wk = p.split, ks = warp % wk, per = 8 / wk;  // wk warps share a tile's inputs
+    const int64_t col0 = (int64_t)blockIdx.y * MR;
+    const int nsl = (int)((p.nb + 7) / 8);
+    const int tiles = (int)((p.n_out + kR - 1) / kR), step = (int)gridDim.x * per;
+    const T* x = static_cast<const T*>(p.x) + col0 * p.n_in;
+    uint4* mine = ring + warp * kDepth * kR * 32 + lane;
+    const int64_t line = p.nb * 4;  // 16-byte units of a row of W
+    const uint32_t magic = held(0x4b000000u);
+
+    // the slice to fetch next: (tile, slice), always kDepth ahead
+    int ft = (int)blockIdx.x * per + warp / wk, fs = ks;
+    const uint4* fp = p.wq + (int64_t)ft * kR * line + (int64_t)fs * 32 + lane;
+    const auto fetch = [&](int at) {
+        const bool in = ft < tiles && (int64_t)fs * 8 + (lane >> 2) < p.nb;
 #pragma unroll
-        for (int i = 0; i < UB; ++i) {
-            const int b = b0 + i * step;
-            qa[i] = qb[i] = make_uint4(0, 0, 0, 0);
-            if (b < nb) {
-                if (oka) qa[i] = __ldg(wa + (int64_t)b * 4);
-                if (okb) qb[i] = __ldg(wb + (int64_t)b * 4);
-            }
-#pragma unroll
-            for (int g = 0; g < GPB; ++g) {
-                const int gi = b * GPB + g;
-                const bool ok = b < nb && gi < p.ng;
-                fa[i][g] = ok && oka ? sa[gi] : bf(0.f);
-                fb[i][g] = ok && okb ? sb[gi] : bf(0.f);
-            }
+        for (int r = 0; r < kR; ++r) {
+            const bool ok = in && (int64_t)ft * kR + r < p.n_out;
+            cp_async16(mine + (at * kR + r) * 32, ok ? fp + r * line : p.wq, ok ? 16 : 0);
+        }
+        cp_async_commit();
+        fs += wk;
+        fp += wk * 32;
+        if (fs >= nsl) {
+            fs = ks;
+            ft += step;
+            fp = p.wq + (int64_t)ft * kR * line + (int64_t)fs * 32 + lane;
         }
     };
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    int b0 = rank * 8 + warp;
-    load(b0);
-    for (; b0 < nb; b0 += UB * step) {
-        uint4 ca[UB], cb[UB];
-        float ga[UB][GPB], gb[UB][GPB];
+    float s[kR][GPB];
+    const auto scales = [&](int tile, int sl) {
+        const int64_t g0 = ((int64_t)sl * 8 + (lane >> 2)) * GPB;
+        const __nv_bfloat16* sc = p.scales + (int64_t)tile * kR * p.ng + g0;
 #pragma unroll
-        for (int i = 0; i < UB; ++i) {
-            ca[i] = qa[i];
-            cb[i] = qb[i];
+        for (int r = 0; r < kR; ++r)
 #pragma unroll
-            for (int g = 0; g < GPB; ++g) {
-                ga[i][g] = __bfloat162float(fa[i][g]);
-                gb[i][g] = __bfloat162float(fb[i][g]);
-            }
+            for (int g = 0; g < GPB; ++g)
+                s[r][g] = g0 + g < p.ng && (int64_t)tile * kR + r < p.n_out
+                              ? __bfloat162float(sc[r * p.ng + g])
+                              : 0.f;
+    };
+    int tile = ft;
+    const int rounds = (tiles - (int)blockIdx.x * per + step - 1) / step;
+    if (ks < nsl) {
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i) fetch(i);
+        scales(tile, ks);
+    }
+    const bool xvec = p.n_in % (16 / sizeof(T)) == 0;
+    for (int e = tid; e < nsl * 128 * MR; e += 256) {  // eight inputs each
+        const int m = e / (nsl * 128), unit = e % (nsl * 128);
+        const int64_t k = unit * 8;
+        float f[8];
+        if (col0 + m < p.m && xvec && k + 8 <= p.n_in) {
+            load8(x + m * p.n_in + k, f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                f[i] = col0 + m < p.m && k + i < p.n_in ? to_f(x[m * p.n_in + k + i]) : 0.f;
         }
-        load(b0 + UB * step);
 #pragma unroll
-        for (int i = 0; i < UB; ++i) {
-            const int b = b0 + i * step;
-            if (b >= nb) break;
-            uint4 v[4];
+        for (int i = 0; i < 8; ++i) f[i] *= 1.f / (1024.f * (float)(1 << (4 * (i / 2))));
+        const int b = unit / 16, j = unit % 16 / 4, c = unit % 4;
+        float4* at = xs + ((m * nsl + b / 8) * 4 + j) * 64 + b % 8 * 4 + c;
+        at[0] = make_float4(f[0], f[1], f[2], f[3]);
+        at[32] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __syncthreads();
+
+    int at = 0;  // place of the present slice in the ring
+    for (int round = 0; round < rounds; ++round, tile += step) {
+        float2 acc[kR][MR];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = b * 128 + 32 * j;
-                v[j] = make_uint4(0, 0, 0, 0);
-                if (okx && k + 8 * c < p.n_in) v[j] = __ldg(reinterpret_cast<const uint4*>(x + k));
+        for (int r = 0; r < kR; ++r)
+#pragma unroll
+            for (int m = 0; m < MR; ++m) acc[r][m] = make_float2(0.f, 0.f);
+        for (int sl = ks; sl < nsl; sl += wk) {
+            uint4 q[kR];
+            float2 cs[kR][GPB];
+            cp_async_wait<kDepth - 1>();
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                q[r] = mine[(at * kR + r) * 32];
+#pragma unroll
+                for (int g = 0; g < GPB; ++g) cs[r][g] = make_float2(s[r][g], s[r][g]);
             }
-            const uint32_t* ua = reinterpret_cast<const uint32_t*>(&ca[i]);
-            const uint32_t* ub = reinterpret_cast<const uint32_t*>(&cb[i]);
-            float part[4];
+            fetch(at);
+            at = at + 1 == kDepth ? 0 : at + 1;
+            if (sl + wk < nsl)
+                scales(tile, sl + wk);
+            else
+                scales(tile + step, ks);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (j % (4 / GPB) == 0) part[0] = part[1] = part[2] = part[3] = 0.f;
-                mma_bf16(part, unpack_pair(ua[j], 0), unpack_pair(ub[j], 0), unpack_pair(ua[j], 1),
-                         unpack_pair(ub[j], 1), v[j].x, v[j].y);
-                mma_bf16(part, unpack_pair(ua[j], 2), unpack_pair(ub[j], 2), unpack_pair(ua[j], 3),
-                         unpack_pair(ub[j], 3), v[j].z, v[j].w);
-                if ((j + 1) % (4 / GPB) == 0) {
-                    const int g = j / (4 / GPB);
-                    acc[0] = fmaf(ga[i][g], part[0], acc[0]);
-                    acc[1] = fmaf(ga[i][g], part[1], acc[1]);
-                    acc[2] = fmaf(gb[i][g], part[2], acc[2]);
-                    acc[3] = fmaf(gb[i][g], part[3], acc[3]);
+                float4 xa[MR], xb[MR];
+#pragma unroll
+                for (int m = 0; m < MR; ++m) {
+                    const float4* xp = xs + ((m * nsl + sl) * 4 + j) * 64 + lane;
+                    xa[m] = xp[0];
+                    xb[m] = xp[32];
+                }
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    const uint32_t word = reinterpret_cast<const uint32_t*>(&q[r])[j];
+                    const uint32_t hi = word >> 16;
+                    const float2 d0 = nibble_pair(word, hi, 0, magic);
+                    const float2 d1 = nibble_pair(word, hi, 1, magic);
+                    const float2 d2 = nibble_pair(word, hi, 2, magic);
+                    const float2 d3 = nibble_pair(word, hi, 3, magic);
+#pragma unroll
+                    for (int m = 0; m < MR; ++m) {
+                        float2 t = __fmul2_rn(d0, make_float2(xa[m].x, xa[m].y));
+                        t = __ffma2_rn(d1, make_float2(xa[m].z, xa[m].w), t);
+                        t = __ffma2_rn(d2, make_float2(xb[m].x, xb[m].y), t);
+                        t = __ffma2_rn(d3, make_float2(xb[m].z, xb[m].w), t);
+                        acc[r][m] = __ffma2_rn(cs[r][j / (4 / GPB)], t, acc[r][m]);
+                    }
                 }
             }
         }
-    }
+        // the lanes' sums: every lane ends up with all of them
+        float v[kR * MR];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) red[warp][c * 2 + (e & 1)][r + (e >> 1) * 8] = acc[e];
-    cg::cluster_group cl = cg::this_cluster();
-    if (p.split > 1)
-        cl.sync();
-    else
-        __syncthreads();
-    for (int e = rank * 256 + tid; e < 128; e += 256 * p.split) {
-        const int row = e % 16, col = e / 16;
-        const int64_t o = row0 + row;
-        if (o >= p.n_out || col >= p.m) continue;
-        float v = 0.f;
-        for (int s = 0; s < p.split; ++s) {
-            const float* from = p.split > 1 ? cl.map_shared_rank(&red[0][0][0], s) : &red[0][0][0];
+        for (int r = 0; r < kR; ++r) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v += from[(k * 8 + col) * 16 + row];
+            for (int m = 0; m < MR; ++m) {
+                float t = acc[r][m].x + acc[r][m].y;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+                v[m * kR + r] = t;
+            }
         }
-        v *= 1024.f;
-        if (p.bias) v += p.bias[o];
-        if (p.residual) v += to_f(static_cast<const bf*>(p.residual)[col * p.n_out + o]);
-        static_cast<bf*>(p.y)[col * p.n_out + o] = from_f<bf>(v);
+        float mysum = 0.f;  // lane m * kR + r
+#pragma unroll
+        for (int i = 0; i < kR * MR; ++i)
+            if (lane == i) mysum = v[i];
+        if (wk > 1) {  // then the wk warps', in fixed order
+            if (lane < kR * MR) red[round & 1][warp][lane % kR][lane / kR] = mysum;
+            __syncthreads();
+            if (ks == 0 && lane < kR * MR) {
+                mysum = 0.f;
+                for (int k = 0; k < wk; ++k)
+                    mysum += red[round & 1][warp + k][lane % kR][lane / kR];
+            }
+        }
+        const int64_t o = (int64_t)tile * kR + lane % kR, col = col0 + lane / kR;
+        if (ks == 0 && lane < kR * MR && o < p.n_out && col < p.m) {
+            float y = mysum * 1024.f;
+            if (p.bias) y += p.bias[o];
+            if (p.residual) y += to_f(static_cast<const T*>(p.residual)[col * p.n_out + o]);
+            static_cast<T*>(p.y)[col * p.n_out + o] = from_f<T>(y);
+        }
     }
-    if (p.split > 1) cl.sync();
+    cp_async_wait<0>();
 }
 
-// Launches clusters of p.split blocks.  `ready`: the devices on which this
-// kernel's attributes are set.
-static cudaError_t w4_launch(void (*kern)(const W4Params), const W4Params& p, dim3 grid, int smem,
-                             std::atomic<uint64_t>& ready, cudaStream_t st) {
-    cudaError_t e = smem_once(reinterpret_cast<const void*>(kern), smem, ready);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)p.split;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
-template <int G>
+template <typename T, int G, int MR>
 static cudaError_t w4_rows(W4Params p, int sms, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
-    const int64_t rt = (p.n_out + 15) / 16;
-    // share the inputs out while the blocks do not fill two per SM and every
-    // warp keeps a block of them
+    const int64_t tiles = (p.n_out + kR - 1) / kR, nsl = (p.nb + 7) / 8;
+    // warps share a tile's inputs while there are fewer than sixteen warps per
+    // SM and each keeps a slice
     p.split = 1;
-    while (p.split < 8 && 16 * p.split <= p.nb && rt * p.split * 2 <= 4LL * sms) p.split *= 2;
-    return w4_launch(w4_rows_kernel<G>, p, dim3((unsigned)(rt * p.split)), 0, ready, st);
+    while (p.split < 8 && 2 * p.split <= nsl && tiles * p.split < 16LL * sms) p.split *= 2;
+    constexpr int ring = 8 * kDepth * kR * 512;
+    const int smem = ring + MR * (int)nsl * 4096;
+    const cudaError_t e = smem_once(reinterpret_cast<const void*>(w4_rows_kernel<T, G, MR>),
+                                    ring + kRowsSlices * 4096, ready);
+    if (e != cudaSuccess) return e;
+    const int64_t per = 8 / p.split;
+    w4_rows_kernel<T, G, MR><<<dim3((unsigned)min64((tiles + per - 1) / per, 2LL * sms),
+                                    (unsigned)((p.m + MR - 1) / MR)), 256, smem, st>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename T, int WR, int WK, int NT, int G>
@@ -491,15 +526,21 @@ static cudaError_t w4_run(W4Params p, int sms, cudaStream_t st) {
     p.split = 1;
     while (p.split < 8 && 2 * p.split <= nch && rt * ct * p.split < 3LL * sms) p.split *= 2;
     static std::atomic<uint64_t> ready{0};
-    return w4_launch(w4_linear_kernel<T, WR, WK, NT, G>, p,
-                     dim3((unsigned)(rt * p.split), (unsigned)ct), smem, ready, st);
+    return w4_launch(w4_linear_kernel<T, WR, WK, NT, G>,
+                     dim3((unsigned)(rt * p.split), (unsigned)ct), 256, smem, p.split, ready, st,
+                     p);
 }
 
 template <typename T, int G>
 static cudaError_t w4_pick(const W4Params& p, int sms, cudaStream_t st) {
+    const char* force = getenv("W4F");
+    const int f = force ? atoi(force) : 0;
     if constexpr (sizeof(T) == 2) {
-        if (p.m <= 8 && p.n_in % 8 == 0) return w4_rows<G>(p, sms, st);
+        if (f == 1 && p.n_in % 8 == 0 && p.n_in >= 64) return launch_w4_tc(p, G, sms, st);
     }
+    const int64_t slices = (p.nb + 7) / 8;  // of one row of x
+    if (f != 2 && p.m == 1 && slices <= kRowsSlices) return w4_rows<T, G, 1>(p, sms, st);
+    if (f != 2 && p.m == 2 && 2 * slices <= kRowsSlices) return w4_rows<T, G, 2>(p, sms, st);
     if (p.m <= 8) return w4_run<T, 1, 8, 1, G>(p, sms, st);
     if (p.m <= 16) return w4_run<T, 2, 4, 2, G>(p, sms, st);
     if (p.m <= 32) return w4_run<T, 4, 2, 4, G>(p, sms, st);
