@@ -310,20 +310,16 @@ __global__ void __launch_bounds__(256) w4_linear_kernel(const W4Params p) {
 }
 
 // One or two rows of x (the decode of one or two sessions: the time is that of
-// reading the weights), on the CUDA cores.  A warp takes kR rows of W (a tile)
-// and 1024 inputs of each (a slice) at a time, 16 bytes a lane, so its loads
-// are whole lines and a value of x serves kR weights.  A nibble becomes a float
-// without a conversion: or-ed into the bits of 2^23 at nibble place i (0 to 3)
-// it reads 2^23 + 16^i q, and a packed addition of two such leaves
-// 16^i (q - 8), exactly; the 16^-i (and the 1 / 1024 of unpack_pair) is in the x
-// that is staged.  A word's eight products are summed unscaled and enter the
-// row's sum with its group's scale.
-// Blocks stay resident: x is staged once, and a warp goes on from tile to tile
-// while its next kDepth slices of W are on their way into its own part of
-// shared memory (cp.async, each lane its own 16 bytes: no barrier).
-constexpr int kR = 4;           // rows of W per tile
-constexpr int kRowsSlices = 32; // most slices of x (all its rows) in shared memory
-constexpr int kDepth = 4;
+// reading the weights), on the CUDA cores.  A warp takes kR rows of W and 1024
+// inputs of each (a slice) at a time, 16 bytes a lane, so its loads are whole
+// lines and a value of x serves kR weights.  A nibble becomes a float without
+// a conversion: or-ed into the bits of 2^23 at nibble place i (0 to 3) it reads
+// 2^23 + 16^i q, and a packed addition of two such leaves 16^i (q - 8),
+// exactly; the 16^-i (and the 1 / 1024 of unpack_pair) is in the x that is
+// staged.  A word's eight products are summed unscaled and enter the row's sum
+// with its group's scale.
+constexpr int kR = 4;           // rows of W per warp
+constexpr int kRowsSlices = 8;  // slices of x in shared memory at a time
 
 // Nibbles i of the two halves of a word (inputs 2 i, 2 i + 1): 16^i (q - 8).
 __device__ __forceinline__ float2 nibble_pair(uint32_t lo, uint32_t hi, int i, uint32_t magic) {
@@ -334,117 +330,101 @@ __device__ __forceinline__ float2 nibble_pair(uint32_t lo, uint32_t hi, int i, u
 }
 
 template <typename T, int G, int MR>
-__global__ void __launch_bounds__(256, 2) w4_rows_kernel(const W4Params p) {
+__global__ void __launch_bounds__(256, 3) w4_rows_kernel(const W4Params p) {
     constexpr int GPB = 128 / G;
     extern __shared__ __align__(16) unsigned char smem[];
-    uint4* ring = reinterpret_cast<uint4*>(smem);  // [warp][kDepth][kR][lane]
-    float4* xs = reinterpret_cast<float4*>(ring + 8 * kDepth * kR * 32);
-    // xs: [row of x][slice][j][half][lane]
-    __shared__ float red[2][8][kR][MR];
+    float4* xs = reinterpret_cast<float4*>(smem);  // [row of x][slice][j][half][lane]
+    __shared__ float red[8][kR][MR];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int wk = p.split, ks = warp % wk, per = 8 / wk;  // wk warps share a tile's inputs
+    const int wk = p.split, ks = warp % wk;  // wk warps share their rows' inputs
+    const int64_t row0 = ((int64_t)blockIdx.x * (8 / wk) + warp / wk) * kR;
     const int64_t col0 = (int64_t)blockIdx.y * MR;
     const int nsl = (int)((p.nb + 7) / 8);
-    const int tiles = (int)((p.n_out + kR - 1) / kR), step = (int)gridDim.x * per;
+    const int slices = min(nsl, kRowsSlices);
     const T* x = static_cast<const T*>(p.x) + col0 * p.n_in;
-    uint4* mine = ring + warp * kDepth * kR * 32 + lane;
-    const int64_t line = p.nb * 4;  // 16-byte units of a row of W
+    // rows past the end read the last one and are not stored
+    const int64_t last = p.n_out - 1;
+    const uint4* w = p.wq + min64(row0, last) * p.nb * 4 + lane;
+    const __nv_bfloat16* sc = p.scales + min64(row0, last) * p.ng;
+    const int rows = (int)min64(kR, p.n_out - row0);
     const uint32_t magic = held(0x4b000000u);
-
-    // the slice to fetch next: (tile, slice), always kDepth ahead
-    int ft = (int)blockIdx.x * per + warp / wk, fs = ks;
-    const uint4* fp = p.wq + (int64_t)ft * kR * line + (int64_t)fs * 32 + lane;
-    const auto fetch = [&](int at) {
-        const bool in = ft < tiles && (int64_t)fs * 8 + (lane >> 2) < p.nb;
+    uint4 q[kR];
+    __nv_bfloat16 s[kR][GPB];
+    const auto load = [&](int sl) {
+        const int b = sl * 8 + (lane >> 2);
+        const uint4* wp = w + (int64_t)sl * 32;
+        const __nv_bfloat16* sp = sc + (int64_t)b * GPB;
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
-            const bool ok = in && (int64_t)ft * kR + r < p.n_out;
-            cp_async16(mine + (at * kR + r) * 32, ok ? fp + r * line : p.wq, ok ? 16 : 0);
-        }
-        cp_async_commit();
-        fs += wk;
-        fp += wk * 32;
-        if (fs >= nsl) {
-            fs = ks;
-            ft += step;
-            fp = p.wq + (int64_t)ft * kR * line + (int64_t)fs * 32 + lane;
-        }
-    };
-    float s[kR][GPB];
-    const auto scales = [&](int tile, int sl) {
-        const int64_t g0 = ((int64_t)sl * 8 + (lane >> 2)) * GPB;
-        const __nv_bfloat16* sc = p.scales + (int64_t)tile * kR * p.ng + g0;
-#pragma unroll
-        for (int r = 0; r < kR; ++r)
+            q[r] = b < p.nb ? __ldg(wp) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int g = 0; g < GPB; ++g)
-                s[r][g] = g0 + g < p.ng && (int64_t)tile * kR + r < p.n_out
-                              ? __bfloat162float(sc[r * p.ng + g])
-                              : 0.f;
-    };
-    int tile = ft;
-    const int rounds = (tiles - (int)blockIdx.x * per + step - 1) / step;
-    if (ks < nsl) {
-#pragma unroll
-        for (int i = 0; i < kDepth; ++i) fetch(i);
-        scales(tile, ks);
-    }
-    const bool xvec = p.n_in % (16 / sizeof(T)) == 0;
-    for (int e = tid; e < nsl * 128 * MR; e += 256) {  // eight inputs each
-        const int m = e / (nsl * 128), unit = e % (nsl * 128);
-        const int64_t k = unit * 8;
-        float f[8];
-        if (col0 + m < p.m && xvec && k + 8 <= p.n_in) {
-            load8(x + m * p.n_in + k, f);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f[i] = col0 + m < p.m && k + i < p.n_in ? to_f(x[m * p.n_in + k + i]) : 0.f;
+                s[r][g] = b * GPB + g < p.ng ? sp[g] : __nv_bfloat16(0.f);
+            if (r + 1 < rows) {
+                wp += p.nb * 4;
+                sp += p.ng;
+            }
         }
+    };
+    float2 acc[kR][MR];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= 1.f / (1024.f * (float)(1 << (4 * (i / 2))));
-        const int b = unit / 16, j = unit % 16 / 4, c = unit % 4;
-        float4* at = xs + ((m * nsl + b / 8) * 4 + j) * 64 + b % 8 * 4 + c;
-        at[0] = make_float4(f[0], f[1], f[2], f[3]);
-        at[32] = make_float4(f[4], f[5], f[6], f[7]);
-    }
-    __syncthreads();
-
-    int at = 0;  // place of the present slice in the ring
-    for (int round = 0; round < rounds; ++round, tile += step) {
-        float2 acc[kR][MR];
+    for (int r = 0; r < kR; ++r)
 #pragma unroll
-        for (int r = 0; r < kR; ++r)
+        for (int m = 0; m < MR; ++m) acc[r][m] = make_float2(0.f, 0.f);
+    if (ks < nsl) load(ks);
+    const bool xvec = p.n_in % (16 / sizeof(T)) == 0;
+    for (int s0 = 0; s0 < nsl; s0 += slices) {
+        const int n = min(slices, nsl - s0);
+        if (s0 > 0) __syncthreads();
 #pragma unroll
-            for (int m = 0; m < MR; ++m) acc[r][m] = make_float2(0.f, 0.f);
-        for (int sl = ks; sl < nsl; sl += wk) {
-            uint4 q[kR];
+        for (int m = 0; m < MR; ++m) {
+            const bool in = col0 + m < p.m;
+            for (int unit = tid; unit < n * 128; unit += 256) {  // eight inputs each
+                const int64_t k = (int64_t)s0 * 1024 + unit * 8;
+                float f[8];
+                if (in && xvec && k + 8 <= p.n_in) {
+                    load8(x + m * p.n_in + k, f);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        f[i] = in && k + i < p.n_in ? to_f(x[m * p.n_in + k + i]) : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] *= 1.f / (1024.f * (float)(1 << (4 * (i / 2))));
+                const int b = unit / 16, j = unit % 16 / 4, c = unit % 4;
+                float4* at = xs + ((m * slices + b / 8) * 4 + j) * 64 + b % 8 * 4 + c;
+                at[0] = make_float4(f[0], f[1], f[2], f[3]);
+                at[32] = make_float4(f[4], f[5], f[6], f[7]);
+            }
+        }
+        __syncthreads();
+        // (slices is a multiple of wk or all of them: a warp's slices go on
+        // from one stage to the next in steps of wk)
+        for (int sl = s0 + ks; sl < s0 + n; sl += wk) {
+            uint4 cq[kR];
             float2 cs[kR][GPB];
-            cp_async_wait<kDepth - 1>();
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
-                q[r] = mine[(at * kR + r) * 32];
+                cq[r] = q[r];
 #pragma unroll
-                for (int g = 0; g < GPB; ++g) cs[r][g] = make_float2(s[r][g], s[r][g]);
+                for (int g = 0; g < GPB; ++g) {
+                    const float f = __bfloat162float(s[r][g]);
+                    cs[r][g] = make_float2(f, f);
+                }
             }
-            fetch(at);
-            at = at + 1 == kDepth ? 0 : at + 1;
-            if (sl + wk < nsl)
-                scales(tile, sl + wk);
-            else
-                scales(tile + step, ks);
+            if (sl + wk < nsl) load(sl + wk);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float4 xa[MR], xb[MR];
 #pragma unroll
                 for (int m = 0; m < MR; ++m) {
-                    const float4* xp = xs + ((m * nsl + sl) * 4 + j) * 64 + lane;
-                    xa[m] = xp[0];
-                    xb[m] = xp[32];
+                    const float4* at = xs + ((m * slices + sl - s0) * 4 + j) * 64 + lane;
+                    xa[m] = at[0];
+                    xb[m] = at[32];
                 }
 #pragma unroll
                 for (int r = 0; r < kR; ++r) {
-                    const uint32_t word = reinterpret_cast<const uint32_t*>(&q[r])[j];
+                    const uint32_t word = reinterpret_cast<const uint32_t*>(&cq[r])[j];
                     const uint32_t hi = word >> 16;
                     const float2 d0 = nibble_pair(word, hi, 0, magic);
                     const float2 d1 = nibble_pair(word, hi, 1, magic);
@@ -461,57 +441,47 @@ __global__ void __launch_bounds__(256, 2) w4_rows_kernel(const W4Params p) {
                 }
             }
         }
-        // the lanes' sums: every lane ends up with all of them
-        float v[kR * MR];
+    }
+    // the lanes' sums, then the wk warps', in fixed order
 #pragma unroll
-        for (int r = 0; r < kR; ++r) {
+    for (int r = 0; r < kR; ++r) {
 #pragma unroll
-            for (int m = 0; m < MR; ++m) {
-                float t = acc[r][m].x + acc[r][m].y;
+        for (int m = 0; m < MR; ++m) {
+            float v = acc[r][m].x + acc[r][m].y;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-                v[m * kR + r] = t;
-            }
-        }
-        float mysum = 0.f;  // lane m * kR + r
-#pragma unroll
-        for (int i = 0; i < kR * MR; ++i)
-            if (lane == i) mysum = v[i];
-        if (wk > 1) {  // then the wk warps', in fixed order
-            if (lane < kR * MR) red[round & 1][warp][lane % kR][lane / kR] = mysum;
-            __syncthreads();
-            if (ks == 0 && lane < kR * MR) {
-                mysum = 0.f;
-                for (int k = 0; k < wk; ++k)
-                    mysum += red[round & 1][warp + k][lane % kR][lane / kR];
-            }
-        }
-        const int64_t o = (int64_t)tile * kR + lane % kR, col = col0 + lane / kR;
-        if (ks == 0 && lane < kR * MR && o < p.n_out && col < p.m) {
-            float y = mysum * 1024.f;
-            if (p.bias) y += p.bias[o];
-            if (p.residual) y += to_f(static_cast<const T*>(p.residual)[col * p.n_out + o]);
-            static_cast<T*>(p.y)[col * p.n_out + o] = from_f<T>(y);
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane == 0) red[warp][r][m] = v;
         }
     }
-    cp_async_wait<0>();
+    __syncthreads();
+    if (ks == 0 && lane < kR * MR) {
+        const int r = lane % kR, m = lane / kR;
+        const int64_t o = row0 + r, col = col0 + m;
+        if (o < p.n_out && col < p.m) {
+            float v = 0.f;
+            for (int k = 0; k < wk; ++k) v += red[warp + k][r][m];
+            v *= 1024.f;
+            if (p.bias) v += p.bias[o];
+            if (p.residual) v += to_f(static_cast<const T*>(p.residual)[col * p.n_out + o]);
+            static_cast<T*>(p.y)[col * p.n_out + o] = from_f<T>(v);
+        }
+    }
 }
 
 template <typename T, int G, int MR>
 static cudaError_t w4_rows(W4Params p, int sms, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
     const int64_t tiles = (p.n_out + kR - 1) / kR, nsl = (p.nb + 7) / 8;
-    // warps share a tile's inputs while there are fewer than sixteen warps per
-    // SM and each keeps a slice
+    // warps share their rows' inputs while there are fewer than sixteen warps
+    // per SM and each keeps a slice
     p.split = 1;
     while (p.split < 8 && 2 * p.split <= nsl && tiles * p.split < 16LL * sms) p.split *= 2;
-    constexpr int ring = 8 * kDepth * kR * 512;
-    const int smem = ring + MR * (int)nsl * 4096;
+    const int smem = MR * (int)min64(nsl, kRowsSlices) * 4096;
     const cudaError_t e = smem_once(reinterpret_cast<const void*>(w4_rows_kernel<T, G, MR>),
-                                    ring + kRowsSlices * 4096, ready);
+                                    MR * kRowsSlices * 4096, ready);
     if (e != cudaSuccess) return e;
     const int64_t per = 8 / p.split;
-    w4_rows_kernel<T, G, MR><<<dim3((unsigned)min64((tiles + per - 1) / per, 2LL * sms),
+    w4_rows_kernel<T, G, MR><<<dim3((unsigned)((tiles + per - 1) / per),
                                     (unsigned)((p.m + MR - 1) / MR)), 256, smem, st>>>(p);
     return cudaGetLastError();
 }
@@ -536,11 +506,10 @@ static cudaError_t w4_pick(const W4Params& p, int sms, cudaStream_t st) {
     const char* force = getenv("W4F");
     const int f = force ? atoi(force) : 0;
     if constexpr (sizeof(T) == 2) {
-        if (f == 1 && p.n_in % 8 == 0 && p.n_in >= 64) return launch_w4_tc(p, G, sms, st);
+        if (f == 1 && p.n_in % 8 == 0 && p.n_in > 128) return launch_w4_tc(p, G, sms, st);
     }
-    const int64_t slices = (p.nb + 7) / 8;  // of one row of x
-    if (f != 2 && p.m == 1 && slices <= kRowsSlices) return w4_rows<T, G, 1>(p, sms, st);
-    if (f != 2 && p.m == 2 && 2 * slices <= kRowsSlices) return w4_rows<T, G, 2>(p, sms, st);
+    if (f != 2 && p.m == 1) return w4_rows<T, G, 1>(p, sms, st);
+    if (f != 2 && p.m == 2) return w4_rows<T, G, 2>(p, sms, st);
     if (p.m <= 8) return w4_run<T, 1, 8, 1, G>(p, sms, st);
     if (p.m <= 16) return w4_run<T, 2, 4, 2, G>(p, sms, st);
     if (p.m <= 32) return w4_run<T, 4, 2, 4, G>(p, sms, st);

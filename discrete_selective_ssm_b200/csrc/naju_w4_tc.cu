@@ -32,12 +32,12 @@ namespace {
 constexpr int kTcThreads = 320;
 constexpr int kTcPolls = 1 << 20;
 
-// Shared memory of a stage: packed weights, then x (N rows x 128 inputs, two
-// 64-column tiles).
+// Shared memory of a stage, two blocks of 128 inputs: packed weights (128 rows
+// of 128 bytes), then x (N rows x 256 inputs, four 64-column tiles).
 template <int N> struct W4Tc {
-    static constexpr int kWBytes = 128 * 64, kXBytes = N * 256;
+    static constexpr int kWBytes = 128 * 128, kXBytes = N * 512;
     static constexpr int kStage = kWBytes + kXBytes;
-    static constexpr int kStages = N <= 32 ? 6 : 4;
+    static constexpr int kStages = N == 16 ? 4 : N == 32 ? 3 : 2;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kRed = N * 128 * 4;  // the sums, over the ring when it is done
     static constexpr int kSmem = (kRing > kRed ? kRing : kRed) + 1024;
@@ -124,13 +124,14 @@ w4_tc_kernel(const __grid_constant__ W4Params p, const __grid_constant__ CUtenso
         const PairBits bits;
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         for (int b = b0; b < b1; ++b) {
-            const int i = b - b0, s = i % S, ab = i & 1;
-            wait_phase(&full[s], (i / S) & 1, &s_bad);
-            const unsigned char* line = ring + s * C::kStage + tid * 64;
+            const int i = b - b0, st = i >> 1, s = st % S, ab = i & 1;
+            if (!(i & 1)) wait_phase(&full[s], (st / S) & 1, &s_bad);
+            const unsigned char* line = ring + s * C::kStage + tid * 128;
             uint4 w[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)  // 64-byte swizzle: chunk ^ (row / 2) % 4
-                w[c] = *reinterpret_cast<const uint4*>(line + ((c ^ ((tid >> 1) & 3)) << 4));
+            for (int c = 0; c < 4; ++c)  // 128-byte swizzle: chunk ^ row % 8
+                w[c] = *reinterpret_cast<const uint4*>(
+                    line + ((((i & 1) * 4 + c) ^ (tid & 7)) << 4));
             uint32_t v[64];  // column: two inputs
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -141,7 +142,7 @@ w4_tc_kernel(const __grid_constant__ W4Params p, const __grid_constant__ CUtenso
                         v[16 * j + 4 * c + q] =
                             unpack_pair(reinterpret_cast<const uint32_t*>(&w[c])[j], q, bits);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
+            if (lane == 0 && ((i & 1) || b + 1 == b1)) mbar_arrive(&empty[s]);
             wait_phase(&aempty[ab], ((i >> 1) & 1) ^ 1, &s_bad);
             fence_after_sync();
             const uint32_t a = tm + lanes + C::kA + ab * 64;
@@ -203,26 +204,29 @@ w4_tc_kernel(const __grid_constant__ W4Params p, const __grid_constant__ CUtenso
             red[(2 * n + 1) * 128 + r] = acc[n].y;
         }
     } else if (warp == 8) {  // --------------------------------------- loader
-        for (int b = b0; b < b1; ++b) {
-            const int i = b - b0, s = i % S;
+        for (int b = b0; b < b1; b += 2) {
+            const int i = (b - b0) >> 1, s = i % S;
             wait_phase(&empty[s], ((i / S) & 1) ^ 1, &s_bad);
             if (lane == 0) {
                 unsigned char* st = ring + s * C::kStage;
                 tma::expect_tx(&full[s], C::kStage);
                 tma::load_3d(st, &wmap, b * 32, (int)row0, 0, &full[s]);
-                tma::load_3d(st + C::kWBytes, &xmap, b * 128, col0, 0, &full[s]);
-                tma::load_3d(st + C::kWBytes + N * 128, &xmap, b * 128 + 64, col0, 0, &full[s]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    tma::load_3d(st + C::kWBytes + q * N * 128, &xmap, b * 128 + q * 64, col0, 0,
+                                 &full[s]);
             }
         }
     } else {  // ------------------------------------------------------ issuer
         constexpr uint32_t idesc = idesc_bf16(128, N);
         int u = 0;
         for (int b = b0; b < b1; ++b) {
-            const int i = b - b0, s = i % S, ab = i & 1;
-            wait_phase(&full[s], (i / S) & 1, &s_bad);
+            const int i = b - b0, st = i >> 1, s = st % S, ab = i & 1;
+            // (the unpackers have seen the stage full before they say so here)
             wait_phase(&afull[ab], (i >> 1) & 1, &s_bad);
             fence_after_sync();
-            const uint32_t xb = smem_u32(ring + s * C::kStage + C::kWBytes);
+            const uint32_t xb =
+                smem_u32(ring + s * C::kStage + C::kWBytes + (i & 1) * N * 256);
             const uint32_t a = tm + C::kA + ab * 64;
 #pragma unroll
             for (int g = 0; g < GPB; ++g, ++u) {
@@ -238,7 +242,7 @@ w4_tc_kernel(const __grid_constant__ W4Params p, const __grid_constant__ CUtenso
                     mma_commit(&dfull[u & 1]);
                     if (g == GPB - 1) {
                         mma_commit(&aempty[ab]);
-                        mma_commit(&empty[s]);
+                        if ((i & 1) || b + 1 == b1) mma_commit(&empty[s]);
                     }
                 }
                 __syncwarp();
@@ -278,7 +282,7 @@ static cudaError_t tc_run(W4Params p, int sms, cudaStream_t st) {
     typedef W4Tc<N> C;
     static std::atomic<uint64_t> ready{0};
     CUtensorMap wmap, xmap;
-    if (!tma_encode_2b_2d_sw64(&wmap, p.wq, p.n_out, p.nb * 32, 128) ||
+    if (!tma_encode_bf16_3d_sw128(&wmap, p.wq, 1, p.n_out, p.nb * 32, 128) ||
         !tma_encode_bf16_3d_sw128(&xmap, p.x, 1, p.m, p.n_in, N))
         return cudaErrorInvalidValue;
     const int64_t rt = (p.n_out + 127) / 128, ct = (p.m + N - 1) / N;
