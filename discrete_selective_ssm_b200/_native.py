@@ -95,6 +95,7 @@ def lib(build_if_missing: bool = True):
             L.naju_testing_bwd_pieces.argtypes = [vp]
             L.naju_testing_bwd_pieces.restype = i32
             L.naju_testing_set_vscan_cluster.argtypes = [i32]
+            L.naju_testing_set_w4_impl.argtypes = [i32]
             L.naju_vscan_workspace_bytes.argtypes = [dp]
             L.naju_vscan_workspace_bytes.restype = sz
             L.naju_vscan_fwd.argtypes = [dp] + [vp] * 8 + [sz, vp]
@@ -595,6 +596,10 @@ def testing_fwd_pieces(dims: Dims) -> int:
 
 def testing_set_vscan_cluster(blocks: int):
     lib().naju_testing_set_vscan_cluster(int(blocks))
+
+
+def testing_set_w4_impl(impl: int):
+    lib().naju_testing_set_w4_impl(int(impl))
 
 
 def testing_set_sm_count(sms: int):

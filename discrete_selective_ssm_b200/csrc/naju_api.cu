@@ -28,6 +28,7 @@ int g_fwd_pieces = 0;  // the same for the tensor-core forward
 int g_fwd_impl = 0;  // 0 automatic, 1 CUDA cores, 2 tensor-core sub-chunk, 3 block form
 int g_bwd_impl = 0;  // 0 automatic, 1 CUDA cores, 2 tensor-core sub-chunk, 3 block form
 int g_vcluster = 0;  // > 0: blocks per unit of the vector-state scan
+int g_w4_impl = 0;   // 0 automatic, 1 warp-level, 2 tcgen05 where it applies
 int g_sm_override = 0;  // > 0: SM count used by the tiling (tests)
 
 // Streaming multiprocessors of the current device, queried once per device
@@ -608,7 +609,7 @@ naju_status naju_w4_linear(int64_t m, int64_t n_in, int64_t n_out, int32_t group
     NAJU_REQUIRE(ok_act(x) && ok_act(wq) && scales && aligned(scales, 2) && ok_act(y));
     NAJU_REQUIRE(ok_opt(residual) && (!bias || aligned(bias, 4)));
     return cuda_status(launch_w4_linear(m, n_in, n_out, group, dtype, x, wq, scales, bias,
-                                        residual, y, sm_count(),
+                                        residual, y, g_w4_impl, sm_count(),
                                         static_cast<cudaStream_t>(stream)));
 }
 
@@ -683,6 +684,7 @@ int32_t naju_testing_bwd_pieces(const void* dims) {
     if (check_dims(dm) != NAJU_OK) return 0;
     return layout(dm).npieces;
 }
+void naju_testing_set_w4_impl(int32_t impl) { g_w4_impl = impl == 1 || impl == 2 ? impl : 0; }
 void naju_testing_set_vscan_cluster(int32_t blocks) {
     g_vcluster = blocks >= 1 && blocks <= 16 ? blocks : 0;
 }

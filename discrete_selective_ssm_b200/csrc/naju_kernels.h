@@ -194,7 +194,8 @@ cudaError_t launch_w4_quantize(int64_t n_out, int64_t n_in, int group, int dtype
                                void* wq, void* scales, cudaStream_t st);
 cudaError_t launch_w4_linear(int64_t m, int64_t n_in, int64_t n_out, int group, int dtype,
                              const void* x, const void* wq, const void* scales, const float* bias,
-                             const void* residual, void* y, int sms, cudaStream_t st);
+                             const void* residual, void* y, int impl, int sms,
+                             cudaStream_t st);
 
 // -------------------------------------------------------- 8-bit state cache
 cudaError_t launch_state_store(int64_t n, int64_t d, int64_t N, int64_t n_slots,

@@ -502,14 +502,21 @@ static cudaError_t w4_run(W4Params p, int sms, cudaStream_t st) {
 }
 
 template <typename T, int G>
-static cudaError_t w4_pick(const W4Params& p, int sms, cudaStream_t st) {
-    const char* force = getenv("W4F");
-    const int f = force ? atoi(force) : 0;
+static cudaError_t w4_pick(const W4Params& p, int impl, int sms, cudaStream_t st) {
+    // One or two rows: CUDA cores (1 x 8192 -> 28672 bf16: 45 us, against 61 for
+    // the warp-level tensor-core form; 1 x 1024 -> 4096: 2.8 and 4.2 us).
+    if (impl == 0 && p.m == 1) return w4_rows<T, G, 1>(p, sms, st);
+    if (impl == 0 && p.m == 2) return w4_rows<T, G, 2>(p, sms, st);
+    // tcgen05 from about 2^28 products on (x in whole tiles of 8 rows): its
+    // blocks take 6 to 8 us to start, share out and add up, the warp-level
+    // form runs at 64 T products a second (64 x 2048 -> 4096: 11 and 22 us,
+    // 16 x 4096 -> 4096: 10.7 and 10.9, 16 x 2048 -> 4096: 9.3 and 5.8).
     if constexpr (sizeof(T) == 2) {
-        if (f == 1 && p.n_in % 8 == 0 && p.n_in > 128) return launch_w4_tc(p, G, sms, st);
+        const bool can = p.n_in % 8 == 0 && p.n_in > 128;
+        const double products = (double)((p.m + 7) / 8 * 8) * (double)p.n_in * (double)p.n_out;
+        if (can && (impl == 2 || (impl == 0 && p.m > 8 && products >= 268435456.0)))
+            return launch_w4_tc(p, G, sms, st);
     }
-    if (f != 2 && p.m == 1) return w4_rows<T, G, 1>(p, sms, st);
-    if (f != 2 && p.m == 2) return w4_rows<T, G, 2>(p, sms, st);
     if (p.m <= 8) return w4_run<T, 1, 8, 1, G>(p, sms, st);
     if (p.m <= 16) return w4_run<T, 2, 4, 2, G>(p, sms, st);
     if (p.m <= 32) return w4_run<T, 4, 2, 4, G>(p, sms, st);
@@ -518,7 +525,8 @@ static cudaError_t w4_pick(const W4Params& p, int sms, cudaStream_t st) {
 
 cudaError_t launch_w4_linear(int64_t m, int64_t n_in, int64_t n_out, int group, int dtype,
                              const void* x, const void* wq, const void* scales, const float* bias,
-                             const void* residual, void* y, int sms, cudaStream_t st) {
+                             const void* residual, void* y, int impl, int sms,
+                             cudaStream_t st) {
     W4Params p{};
     p.x = x;
     p.wq = static_cast<const uint4*>(wq);
@@ -533,10 +541,10 @@ cudaError_t launch_w4_linear(int64_t m, int64_t n_in, int64_t n_out, int group, 
     p.ng = (n_in + group - 1) / group;
     const bool f32 = dtype == NAJU_F32;
     if (group == 32)
-        return f32 ? w4_pick<float, 32>(p, sms, st) : w4_pick<__nv_bfloat16, 32>(p, sms, st);
+        return f32 ? w4_pick<float, 32>(p, impl, sms, st) : w4_pick<__nv_bfloat16, 32>(p, impl, sms, st);
     if (group == 64)
-        return f32 ? w4_pick<float, 64>(p, sms, st) : w4_pick<__nv_bfloat16, 64>(p, sms, st);
-    return f32 ? w4_pick<float, 128>(p, sms, st) : w4_pick<__nv_bfloat16, 128>(p, sms, st);
+        return f32 ? w4_pick<float, 64>(p, impl, sms, st) : w4_pick<__nv_bfloat16, 64>(p, impl, sms, st);
+    return f32 ? w4_pick<float, 128>(p, impl, sms, st) : w4_pick<__nv_bfloat16, 128>(p, impl, sms, st);
 }
 
 }  // namespace naju

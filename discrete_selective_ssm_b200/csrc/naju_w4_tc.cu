@@ -80,7 +80,7 @@ __device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t phase, int* b
 }  // namespace
 
 template <int G, int N>
-__global__ void __launch_bounds__(kTcThreads)
+__global__ void __launch_bounds__(kTcThreads, N <= 64 ? 2 : 1)
 w4_tc_kernel(const __grid_constant__ W4Params p, const __grid_constant__ CUtensorMap wmap,
              const __grid_constant__ CUtensorMap xmap) {
     typedef W4Tc<N> C;
@@ -265,7 +265,7 @@ w4_tc_kernel(const __grid_constant__ W4Params p, const __grid_constant__ CUtenso
         const int64_t o = row0 + e % 128, m = col0 + e / 128;
         if (o >= p.n_out || m >= p.m) continue;
         float v = 0.f;
-        for (int s = 0; s < p.split; ++s) {
+        for (int s = 0; s < p.split; ++s) {  // in fixed order
             v += p.split > 1 ? cl.map_shared_rank(red, s)[e] : red[e];
             if (p.split > 1 ? *cl.map_shared_rank(&s_bad, s) : s_bad) v = NAN;
         }
@@ -287,6 +287,7 @@ static cudaError_t tc_run(W4Params p, int sms, cudaStream_t st) {
         return cudaErrorInvalidValue;
     const int64_t rt = (p.n_out + 127) / 128, ct = (p.m + N - 1) / N;
     const int64_t slots = (N <= 64 ? 2 : 1) * (int64_t)sms;
+    p.split = 1;
     // Blocks per row tile: the fewest rounds of blocks, each as long as its
     // share of the inputs plus what a block takes to start and to add up
     // (about eight blocks of inputs).

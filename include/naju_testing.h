@@ -92,6 +92,11 @@ int32_t naju_testing_bwd_impl(const void* dims);
  * directions: 1 to 16; any other value: automatic. */
 void naju_testing_set_vscan_cluster(int32_t blocks);
 
+/* Kernel of naju_w4_linear: 0 = automatic, 1 = the warp-level tensor-core form,
+ * 2 = the tcgen05 form where it applies (bf16 x, n_in a multiple of 8 above
+ * 128), the warp-level one elsewhere. */
+void naju_testing_set_w4_impl(int32_t impl);
+
 /* Self-test of the tensor-core building block of the tensor-core scans:
  * D[128 x N] = A[128 x K] * B[N x K]^T (device pointers, row-major fp32)
  * computed with A in tensor memory, B in shared memory and kind::tf32 MMAs

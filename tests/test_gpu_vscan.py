@@ -327,3 +327,34 @@ def test_refusals_on_device_tensors():
     with pytest.raises(naju.NajuError):
         naju.vscan_fwd(t["h"], t["a"], workspace=torch.empty(256, dtype=torch.uint8,
                                                              device="cuda"))
+
+
+@pytest.mark.parametrize("cluster", [1, 2, 3, 4, 8, 13, 16])
+def test_blocks_per_unit(cluster):
+    """Every cluster size walks the same items: more blocks than items, a last
+    round that is not full, and one block alone."""
+    naju.testing_set_vscan_cluster(cluster)
+    try:
+        check(make(1, 700, 72, "bf16", seed=cluster))
+        check(make(2, 33, 31, "f32", seed=cluster, coupled=True))
+    finally:
+        naju.testing_set_vscan_cluster(0)
+
+
+def test_the_cluster_size_changes_no_more_than_rounding():
+    t = make(1, 1500, 64, "f32", seed=30)
+    naju.testing_set_vscan_cluster(1)
+    try:
+        one = run(t)
+    finally:
+        naju.testing_set_vscan_cluster(0)
+    many = run(t)
+    by, _, bg = bounds(t)
+    near(many[0], ref.f64(one[0]), 2 * factor(t) * by, "y")
+    near(many[2]["da"], ref.f64(one[2]["da"]), 4 * factor(t) * bg["da"], "da")
+
+
+def test_long_rows_of_every_width_path():
+    """Widths without 16-byte rows take the plain loads, in both directions."""
+    for d, dt in ((65, "bf16"), (66, "bf16"), (33, "f32")):
+        check(make(1, 900, d, dt, seed=d))

@@ -203,3 +203,54 @@ def test_refusals():
         naju.w4_linear(x.half(), wq, scales)
     with pytest.raises(ValueError):
         naju.w4_linear(x, wq, scales, bias=torch.zeros(15, device="cuda"))
+
+
+@pytest.fixture(params=[1, 2], ids=["warp", "tcgen05"])
+def impl(request):
+    naju.testing_set_w4_impl(request.param)
+    yield request.param
+    naju.testing_set_w4_impl(0)
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("m", [1, 2, 15, 16, 17, 32, 33, 64, 65, 128, 129, 300])
+def test_each_form_rows(impl, m, G):
+    x, _, wq, scales = make(m, 520, 200, G, "bf16", m + G + 1)
+    check(x, wq, scales, G)
+
+
+@pytest.mark.parametrize("K", [136, 256, 264, 384, 1000, 1920, 4096])
+@pytest.mark.parametrize("O", [1, 127, 128, 129, 400])
+def test_each_form_sizes(impl, K, O):
+    for m, G in ((5, 128), (40, 32)):
+        x, _, wq, scales = make(m, K, O, G, "bf16", K + O)
+        bias = torch.randn(O, device="cuda")
+        res = torch.randn(m, O, device="cuda").bfloat16()
+        y = check(x, wq, scales, G, bias=bias, residual=res)
+        assert torch.equal(y, naju.w4_linear(x, wq, scales, G, bias=bias, residual=res))
+
+
+def test_each_form_extremes(impl):
+    """The largest bf16 values stay finite until the result, a NaN scale and an
+    infinite input reach their own results only."""
+    x, _, wq, scales = make(20, 512, 160, 128, "bf16", 3)
+    W = weights(wq, scales, 512, 128)
+    x.zero_()
+    x[1, 4] = 3.0e38
+    scales[7, 2] = math.nan
+    x[3, 100] = math.inf
+    y = naju.w4_linear(x, wq, scales, 128).double().cpu().numpy()
+    for o in range(160):
+        if o == 7:
+            assert np.isnan(y[:, o]).all()
+            continue
+        want = float(x[1, 4]) * W[o, 4]
+        assert abs(y[1, o] - want) <= 2.0 ** -8 * abs(want)
+        w = W[o, 100]
+        assert np.isnan(y[3, o]) if w == 0 else y[3, o] == math.copysign(math.inf, w)
+        assert (y[[0, 2] + list(range(4, 20)), o] == 0).all()
+
+
+def test_large_batch_takes_the_tensor_cores():
+    x, _, wq, scales = make(256, 1024, 1100, 64, "bf16", 21)
+    check(x, wq, scales, 64)
