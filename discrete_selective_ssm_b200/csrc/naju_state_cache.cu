@@ -11,20 +11,33 @@
 
 namespace naju {
 
-constexpr int kBatch = 4;
+constexpr int kBatch = 8;
 constexpr int kCacheThreads = 256;
 
-// round(x / s), exactly, for 2^-126 <= s and |x| up to a few hundred s:
-// x * (1 / s) lands within one of it, and the remainder x - q s of that guess
-// is exact in fp32 (a multiple of the smaller of x's and s's last places, and
-// at most about s), so comparing it with s / 2 settles the last step.
-__device__ __forceinline__ float quant1(float x, float s, float inv) {
-    float q = rintf(x * inv);
+// round(x / s) and the scale, exactly.
+//
+// x / s for s in the normal range: t = x (1 / s) + 1.5 2^23, in one rounding,
+// holds round(x / s) in its low bits (two's complement) unless the quotient
+// lies within the product's error of a middle between two integers.  Those are
+// rare (|remainder| above 0.4999 quanta: one value in five thousand) and go
+// through quant_exact: the remainder x - q s of a guess q within one is exact
+// in fp32 (a multiple of the smaller of x's and s's last places, and at most
+// about s), so comparing it with s / 2 settles the last step.  (The conversion
+// instructions run at an eighth of the adder's rate; the sum above costs none.)
+constexpr float kMagic = 12582912.f;  // 1.5 2^23
+
+__device__ __noinline__ int quant_exact(float x, float s) {
+    // below the normal range both sides are scaled up by 2^24, exactly
+    if (s < 1.17549435e-38f) {
+        x *= 16777216.f;
+        s *= 16777216.f;
+    }
+    float q = rintf(__fdiv_rn(x, s));
     const float r = fmaf(-q, s, x);
     const float over = fabsf(r) + fabsf(r) - s;
     // past the middle: one further; on it: the even one of the two
     if (over > 0.f || (over == 0.f && ((int)q & 1))) q += copysignf(1.f, r);
-    return fminf(fmaxf(q, -127.f), 127.f);
+    return (int)fminf(fmaxf(q, -127.f), 127.f);
 }
 
 // Rows are numbered place * d + channel.
@@ -34,18 +47,7 @@ state_store_kernel(int64_t n, int64_t d, int64_t n_slots, const float* __restric
                    const int* __restrict__ slots, int8_t* __restrict__ pool_q,
                    float* __restrict__ pool_scale) {
     constexpr int Q = N / 4, RPI = 32 / Q;  // lanes per row, rows per instruction
-    __shared__ int s_slot;
     const int64_t place = blockIdx.y;
-    // a slot named again by a later place is that place's to store
-    if (threadIdx.x == 0) s_slot = 1;
-    __syncthreads();
-    const int slot = slots[place];
-    bool again = slot < 0 || slot >= n_slots;
-    for (int64_t i = place + 1 + threadIdx.x; i < n && !again; i += kCacheThreads)
-        again = slots[i] == slot;
-    if (again) s_slot = 0;
-    __syncthreads();
-    if (!s_slot) return;
     const int lane = threadIdx.x & 31, ql = lane % Q;
     const int64_t warp = (int64_t)blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
     const int64_t c0 = warp * RPI * kBatch + lane / Q;
@@ -56,30 +58,45 @@ state_store_kernel(int64_t n, int64_t d, int64_t n_slots, const float* __restric
         x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (c < d) x[k] = __ldcs(reinterpret_cast<const float4*>(state + (place * d + c) * N) + ql);
     }
+    // meanwhile: a slot named again by a later place is that place's to store
+    const int slot = slots[place];
+    bool skip = slot < 0 || slot >= n_slots;
+    for (int64_t i = place + 1 + threadIdx.x; i < n && !skip; i += kCacheThreads)
+        skip = slots[i] == slot;
+    if (__syncthreads_or(skip)) return;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
         const int64_t c = c0 + k * RPI;
         const float4 v = x[k];
-        float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-        // (fmaxf drops a NaN: an infinity stands for whatever is not finite)
-        if (!(fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY &&
-              fabsf(v.w) < INFINITY))
-            m = INFINITY;
+        const float e[4] = {v.x, v.y, v.z, v.w};
+        // the largest magnitude as bits: infinities and NaN sort above the rest
+        unsigned m = 0;
 #pragma unroll
-        for (int o = 1; o < Q; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float s = m < INFINITY ? __fdiv_rn(m, 127.f) : NAN;
-        char4 q = make_char4(0, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(e[i]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 1; o < Q; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float s = m < 0x7f800000u ? __fdiv_rn(__uint_as_float(m), 127.f) : NAN;
+        uint32_t q = 0;
         if (s > 0.f) {
-            // below the normal range both sides are scaled up by 2^24, exactly
-            const float up = s < 1.17549435e-38f ? 16777216.f : 1.f, t = s * up;
-            const float inv = __fdiv_rn(1.f, t);
-            q = make_char4(
-                (signed char)quant1(v.x * up, t, inv), (signed char)quant1(v.y * up, t, inv),
-                (signed char)quant1(v.z * up, t, inv), (signed char)quant1(v.w * up, t, inv));
+            const float inv = rcpa_(s);
+            uint32_t t[4];
+            float far = s < 1.17549435e-38f ? 1.f : 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float f = fmaf(e[i], inv, kMagic);
+                t[i] = __float_as_uint(f);
+                far = fmaxf(far, fabsf(fmaf(e[i], inv, kMagic - f)));
+            }
+            if (far > 0.4999f) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t[i] = (uint32_t)quant_exact(e[i], s);
+            }
+            q = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040),
+                            0x5410);
         }
         if (c < d) {
             const int64_t row = (int64_t)slot * d + c;
-            reinterpret_cast<char4*>(pool_q + row * N)[ql] = q;
+            reinterpret_cast<uint32_t*>(pool_q + row * N)[ql] = q;
             if (ql == 0) pool_scale[row] = s;
         }
     }
@@ -97,25 +114,31 @@ state_load_kernel(int64_t d, int64_t n_slots, const int8_t* __restrict__ pool_q,
     const int lane = threadIdx.x & 31, ql = lane % Q;
     const int64_t warp = (int64_t)blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
     const int64_t c0 = warp * RPI * kBatch + lane / Q;
-    char4 q[kBatch];
+    uint32_t q[kBatch];
     float s[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
         const int64_t c = c0 + k * RPI;
-        q[k] = make_char4(0, 0, 0, 0);
+        q[k] = 0;
         s[k] = 0.f;
         if (live && c < d) {
             const int64_t row = (int64_t)slot * d + c;
-            q[k] = __ldg(reinterpret_cast<const char4*>(pool_q + row * N) + ql);
+            q[k] = __ldg(reinterpret_cast<const uint32_t*>(pool_q + row * N) + ql);
             s[k] = __ldg(pool_scale + row);
         }
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
         const int64_t c = c0 + k * RPI;
+        // a byte as a float: q + 128 in the low bits of 2^23
+        const uint32_t u = q[k] ^ 0x80808080u;
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = s[k] * (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 | i)) - 8388736.f);
         if (c < d)
             reinterpret_cast<float4*>(state + (place * d + c) * N)[ql] =
-                make_float4(s[k] * q[k].x, s[k] * q[k].y, s[k] * q[k].z, s[k] * q[k].w);
+                make_float4(f[0], f[1], f[2], f[3]);
     }
 }
 

@@ -37,12 +37,13 @@ constexpr int kTcPolls = 1 << 20;
 template <int N> struct W4Tc {
     static constexpr int kWBytes = 128 * 128, kXBytes = N * 512;
     static constexpr int kStage = kWBytes + kXBytes;
-    static constexpr int kStages = N == 16 ? 4 : N == 32 ? 3 : 2;
+    static constexpr int kStages = N == 16 ? 4 : N == 32 ? 3 : 2;  // two blocks on an SM
     static constexpr int kRing = kStages * kStage;
     static constexpr int kRed = N * 128 * 4;  // the sums, over the ring when it is done
     static constexpr int kSmem = (kRing > kRed ? kRing : kRed) + 1024;
     // tensor memory: two accumulators, two A blocks (128 bf16 = 64 columns)
-    static constexpr int kA = 2 * N, kCols = 2 * N + 128 > 256 ? 512 : 256;
+    static constexpr int kA = 2 * N, kCols = 256;
+    static_assert(2 * N + 128 <= kCols, "two blocks share an SM's 512 columns");
 };
 
 // D[tmem] (+)= A[tmem] * B[smem]^T, one K = 16 step of bf16 operands.
@@ -80,7 +81,7 @@ __device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t phase, int* b
 }  // namespace
 
 template <int G, int N>
-__global__ void __launch_bounds__(kTcThreads, N <= 64 ? 2 : 1)
+__global__ void __launch_bounds__(kTcThreads, 2)
 w4_tc_kernel(const __grid_constant__ W4Params p, const __grid_constant__ CUtensorMap wmap,
              const __grid_constant__ CUtensorMap xmap) {
     typedef W4Tc<N> C;
@@ -286,7 +287,7 @@ static cudaError_t tc_run(W4Params p, int sms, cudaStream_t st) {
         !tma_encode_bf16_3d_sw128(&xmap, p.x, 1, p.m, p.n_in, N))
         return cudaErrorInvalidValue;
     const int64_t rt = (p.n_out + 127) / 128, ct = (p.m + N - 1) / N;
-    const int64_t slots = (N <= 64 ? 2 : 1) * (int64_t)sms;
+    const int64_t slots = 2 * (int64_t)sms;
     p.split = 1;
     // Blocks per row tile: the fewest rounds of blocks, each as long as its
     // share of the inputs plus what a block takes to start and to add up
@@ -308,8 +309,7 @@ template <int G>
 static cudaError_t tc_pick(const W4Params& p, int sms, cudaStream_t st) {
     if (p.m <= 16) return tc_run<G, 16>(p, sms, st);
     if (p.m <= 32) return tc_run<G, 32>(p, sms, st);
-    if (p.m <= 64) return tc_run<G, 64>(p, sms, st);
-    return tc_run<G, 128>(p, sms, st);
+    return tc_run<G, 64>(p, sms, st);  // (128 at a time: no faster, 256 x 2048 -> 4096)
 }
 
 cudaError_t launch_w4_tc(const W4Params& p, int group, int sms, cudaStream_t st) {
