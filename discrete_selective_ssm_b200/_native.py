@@ -318,6 +318,9 @@ def scan_step_conv(state, conv_state, u, a, b, B, C, conv_w, conv_b=None, z=None
 
 
 # ------------------------------------------------------- vector-state scan
+_C = torch._C
+
+
 def _arg(t, name: str, shape, dtype, device):
     """Data pointer of an argument that must be a contiguous `dtype` tensor of
     `shape` on the CUDA device number `device` (None passes through)."""
@@ -344,22 +347,14 @@ def _cuda_index(t, name: str) -> int:
 def _launch(fn, device: int, stream, *args):
     """fn(*args, raw stream) with CUDA device number `device` current; `stream`
     defaults to that device's current one."""
-    raw = _raw_stream(device) if stream is None else stream.cuda_stream
-    if _get_device() == device:
+    raw = _C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if _C._cuda_getDevice() == device:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(device):
             st = fn(*args, raw)
     if st:
         raise NajuError(st, fn.__name__)
-
-
-def _raw_stream(device: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(device)
-
-
-def _get_device() -> int:
-    return torch._C._cuda_getDevice()
 
 
 def _vdims(h, out_dtype) -> Dims:
@@ -369,14 +364,15 @@ def _vdims(h, out_dtype) -> Dims:
     return Dims(*h.shape, 1, 0, dt, dt if out_dtype is None else out_dtype, 0)
 
 
-def vscan_workspace(dims: Dims, device) -> torch.Tensor:
-    """A workspace of vscan_fwd and vscan_bwd (contents undefined)."""
+def vscan_workspace(dims: Dims, like: torch.Tensor) -> torch.Tensor:
+    """A workspace of vscan_fwd and vscan_bwd on the device of `like`
+    (contents undefined)."""
     n = lib().naju_vscan_workspace_bytes(ctypes.byref(dims))
     if n == 0:
         raise NajuError(1, "naju_vscan_workspace_bytes")
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws = like.new_empty(n, dtype=torch.uint8)
     if ws.data_ptr() % 256:  # (an allocator that aligns less than CUDA's)
-        ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
+        ws = like.new_empty(n + 256, dtype=torch.uint8)
         off = (-ws.data_ptr()) % 256
         ws = ws[off:off + n]
     return ws
@@ -398,11 +394,11 @@ def vscan_fwd(h, a, b=None, *, z=None, x0=None, out_dtype=None, workspace=None, 
     st, ot = (act[0], act[2]), _torch_dt(dims.out_dtype)
     L = _lib or lib()
     if workspace is None:
-        workspace = vscan_workspace(dims, h.device)
+        workspace = vscan_workspace(dims, h)
     if y is None:
         y = torch.empty_like(h, dtype=ot)
     if x_final is None and want_final:
-        x_final = torch.empty(st, dtype=f32, device=h.device)
+        x_final = h.new_empty(st, dtype=f32)
     _launch(L.naju_vscan_fwd, dev, stream, ctypes.byref(dims), _arg(h, "h", act, dt, dev),
             _arg(a, "a", act, dt, dev), _arg(b, "b", act, dt, dev), _arg(z, "z", act, dt, dev),
             _arg(x0, "x0", st, f32, dev), _arg(y, "y", act, ot, dev),
@@ -423,7 +419,7 @@ def vscan_bwd(dy, h, a, b, workspace, *, z=None, dx_final=None, out_dtype=None, 
         grads = {"dh": torch.empty_like(h, dtype=ot), "da": torch.empty_like(h, dtype=ot),
                  "db": None if b is None else torch.empty_like(h, dtype=ot),
                  "dz": None if z is None else torch.empty_like(h, dtype=ot),
-                 "dx0": torch.empty(st, dtype=f32, device=h.device) if want_dx0 else None}
+                 "dx0": h.new_empty(st, dtype=f32) if want_dx0 else None}
     g = grads
     _launch(L.naju_vscan_bwd, dev, stream, ctypes.byref(dims), _arg(h, "h", act, dt, dev),
             _arg(a, "a", act, dt, dev), _arg(b, "b", act, dt, dev), _arg(z, "z", act, dt, dev),
@@ -483,7 +479,7 @@ def w4_linear(x, wq, scales, group=128, bias=None, residual=None, y=None, stream
     out = (*sh[:-1], O)
     L = _lib or lib()
     if y is None:
-        y = torch.empty(out, dtype=dt, device=x.device)
+        y = x.new_empty(out)
     _launch(L.naju_w4_linear, dev, stream, x.numel() // K if K else 0, K, O, group, code,
             _arg(x, "x", sh, dt, dev), _arg(wq, "wq", (O, -(-K // 128) * 64), torch.uint8, dev),
             _arg(scales, "scales", (O, -(-K // group)), torch.bfloat16, dev),
@@ -528,7 +524,7 @@ def state_load(pool_q, pool_scale, slots, state=None, stream=None):
     the pool give a zero state.  Returns state [n, d_inner, d_state] fp32."""
     dev, sizes, q, sc, sl = _cache_args(pool_q, pool_scale, slots)
     if state is None:
-        state = torch.empty(sizes[:3], dtype=torch.float32, device=pool_q.device)
+        state = pool_scale.new_empty(sizes[:3])
     _launch((_lib or lib()).naju_state_load, dev, stream, *sizes, q, sc, sl,
             _arg(state, "state", sizes[:3], torch.float32, dev))
     return state
