@@ -138,7 +138,8 @@ class NajuBlock:
 
     def quantize(self, group: int = 128) -> None:
         """Lays the projections out in 4 bits with one scale per `group` inputs;
-        step() then reads those (training keeps the full weights)."""
+        step() then reads those.  The full weights stay as they are (forward,
+        prefill and backward use them); after they change, call this again."""
         p = self.p
         mats = {"W_in": p["W_in"], "W_a": p["W_a"], "W_out": p["W_out"]}
         if not self.coupled:
@@ -176,7 +177,9 @@ class NajuBlock:
             bc = self._project("W_BC", h)
             y = nj.scan_step(state["state"], h, a, b, bc[:, :self.d_state].contiguous(),
                              bc[:, self.d_state:].contiguous(), z, p["D"])
-        return self._project("W_out", y, residual=x.to(dt)).to(x.dtype)
+        if x.dtype == dt:
+            return self._project("W_out", y, residual=x)
+        return (xf + self._project("W_out", y).float()).to(x.dtype)
 
 
 def init_params(d_model: int, d_inner: int, d_state: int, seed: int = 0) -> dict:

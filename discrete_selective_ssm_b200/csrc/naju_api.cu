@@ -607,7 +607,7 @@ naju_status naju_w4_linear(int64_t m, int64_t n_in, int64_t n_out, int32_t group
     if (st != NAJU_OK) return st;
     NAJU_REQUIRE(m >= 1 && m <= (1 << 20));
     NAJU_REQUIRE(ok_act(x) && ok_act(wq) && scales && aligned(scales, 2) && ok_act(y));
-    NAJU_REQUIRE(ok_opt(residual) && (!bias || aligned(bias, 4)));
+    NAJU_REQUIRE(ok_opt(residual) && (!bias || aligned(bias, 4)) && y != x);
     return cuda_status(launch_w4_linear(m, n_in, n_out, group, dtype, x, wq, scales, bias,
                                         residual, y, g_w4_impl, sm_count(),
                                         static_cast<cudaStream_t>(stream)));

@@ -176,3 +176,21 @@ def test_bf16_gradients_of_the_vector_block_run():
     assert set(g) == set(VECTOR_PARAMS)
     for t in (out, dx, *g.values()):
         assert bool(torch.isfinite(t.float()).all())
+
+
+def test_a_wider_residual_keeps_its_bits():
+    """fp32 inputs to a bf16 block: the residual is added in fp32, as in forward."""
+    blk = NajuBlock(64, 128, 16, "cuda", seed=10)
+    x = torch.randn(2, 1, 64, device="cuda")
+    out, _ = blk.forward(x)
+    for quantised in (False, True):
+        if quantised:
+            blk.quantize()
+        y = blk.step(x[:, 0].contiguous(), blk.new_state(2))
+        assert y.dtype == torch.float32
+        # what the block adds is rounded to bf16, the sum is not
+        added = (y - x[:, 0]).double().cpu().numpy()
+        assert float(np.abs((x[:, 0] + (y - x[:, 0]).bfloat16() - y).cpu().numpy()).max()) <= 1e-6
+        if not quantised:
+            assert_close(y, out[:, 0].cpu().numpy(), 1e-2, name="out")
+        assert np.abs(added).max() > 0

@@ -358,3 +358,40 @@ def test_long_rows_of_every_width_path():
     """Widths without 16-byte rows take the plain loads, in both directions."""
     for d, dt in ((65, "bf16"), (66, "bf16"), (33, "f32")):
         check(make(1, 900, d, dt, seed=d))
+
+
+@pytest.mark.parametrize("d,dtype", [(8, "bf16"), (16, "bf16"), (24, "bf16"), (4, "f32"),
+                                     (8, "f32"), (36, "f32")])
+def test_rows_narrower_than_a_tile(d, dtype):
+    check(make(2, 100, d, dtype, seed=d))
+
+
+def test_batches_of_short_sequences():
+    """Many units of one item or less (the whole batch in one round)."""
+    check(make(200, 5, 72, "bf16", seed=40))
+    check(make(300, 1, 33, "f32", seed=41, coupled=True))
+
+
+def test_two_workspaces_at_once():
+    """Two streams with a workspace each; one workspace used by one call after
+    the other."""
+    s, t = make(2, 800, 64, "f32", seed=42), make(2, 800, 64, "f32", seed=43)
+    want = [run(s), run(t)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for q in streams:
+        q.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        got = []
+        for v, q in zip((s, t), streams):
+            with torch.cuda.stream(q):
+                y, xf, ws = naju.vscan_fwd(v["h"], v["a"], v["b"], z=v["z"], x0=v["x0"])
+                g = naju.vscan_bwd(v["dy"], v["h"], v["a"], v["b"], ws, z=v["z"],
+                                   dx_final=v["dx_final"])
+                got.append((y, xf, g))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[2]["da"], b[2]["da"])
+    _, _, ws = naju.vscan_fwd(s["h"], s["a"], s["b"], z=s["z"], x0=s["x0"])
+    y, _, ws2 = naju.vscan_fwd(t["h"], t["a"], t["b"], z=t["z"], x0=t["x0"], workspace=ws)
+    g = naju.vscan_bwd(t["dy"], t["h"], t["a"], t["b"], ws, z=t["z"], dx_final=t["dx_final"])
+    assert ws2 is ws and torch.equal(y, want[1][0]) and torch.equal(g["dh"], want[1][2]["dh"])

@@ -254,3 +254,35 @@ def test_each_form_extremes(impl):
 def test_large_batch_takes_the_tensor_cores():
     x, _, wq, scales = make(256, 1024, 1100, 64, "bf16", 21)
     check(x, wq, scales, 64)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m", [1, 2])
+@pytest.mark.parametrize("K,O", [(8193, 9), (9216, 700), (20000, 33), (33000, 5)])
+def test_inputs_longer_than_the_stage(m, K, O, dtype):
+    """One and two rows of x that come into shared memory in several parts."""
+    x, _, wq, scales = make(m, K, O, 128, dtype, K + m)
+    check(x, wq, scales, 128)
+
+
+def test_result_over_its_input_is_refused():
+    x, _, wq, scales = make(1, 128, 128, 128, "bf16")
+    with pytest.raises(naju.NajuError):
+        naju.w4_linear(x, wq, scales, y=x)
+
+
+def test_two_calls_at_once():
+    """Two streams, the same weights: neither call keeps anything of its own."""
+    a, _, wq, scales = make(200, 1024, 2048, 64, "bf16", 31)
+    b = torch.randn(200, 1024, device="cuda").bfloat16()
+    want = [naju.w4_linear(t, wq, scales, 64) for t in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        got = []
+        for t, s in zip((a, b), streams):
+            with torch.cuda.stream(s):
+                got.append(naju.w4_linear(t, wq, scales, 64))
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -107,7 +107,8 @@ def test_w4_refusals(L):
     assert q(8, 64, 32, 3, FAKE, FAKE, FAKE) == 2
     assert q(8, 64, 32, 0, None, FAKE, FAKE) == 1
     assert q(8, 64, 32, 0, FAKE, MIS, FAKE) == 1
-    f = lambda *a: L.naju_w4_linear(*a, None)  # noqa: E731
+    out = ctypes.c_void_p(8192)
+    f = lambda *a: L.naju_w4_linear(*a[:-1], out if a[-1] is FAKE else a[-1], None)  # noqa: E731
     #        m  in  out  G  dt  x     wq    s     bias  res   y
     assert f(0, 64, 8, 32, 0, FAKE, FAKE, FAKE, None, None, FAKE) == 1
     assert f(1 << 21, 64, 8, 32, 0, FAKE, FAKE, FAKE, None, None, FAKE) == 1
@@ -119,6 +120,8 @@ def test_w4_refusals(L):
     assert f(1, 64, 8, 32, 0, FAKE, FAKE, None, None, None, FAKE) == 1
     assert f(1, 64, 8, 32, 0, FAKE, FAKE, FAKE, None, MIS, FAKE) == 1
     assert f(1, 64, 8, 32, 0, FAKE, FAKE, FAKE, None, None, None) == 1
+    # the result over the input it is computed from
+    assert L.naju_w4_linear(1, 64, 64, 32, 0, FAKE, FAKE, FAKE, None, None, FAKE, None) == 1
 
 
 def test_w4_binding_refusals():
