@@ -158,3 +158,16 @@ def test_a_session_parked_and_resumed():
     # half a quantum of every state value, decayed and read out; 1e-5: fp32 sums
     assert bool((err <= allow + 1e-5 * (1 + y1.double().abs()[order])).all())
     assert float(np.abs(np.asarray(err.cpu())).max()) > 0
+
+
+def test_offsets_past_32_bits():
+    d, N, S = 2048, 64, 16500
+    assert S * d * N > 2 ** 31
+    pq, ps = naju.state_pool(S, d, N, "cuda")
+    x = states(2, d, N, 12)
+    slots = torch.tensor([S - 1, 16390], dtype=torch.int32, device="cuda")
+    naju.state_store(x, slots, pq, ps)
+    q, s = reference(x)
+    assert torch.equal(pq[slots.long()].cpu(), q) and torch.equal(ps[slots.long()].cpu(), s)
+    assert torch.equal(naju.state_load(pq, ps, slots).cpu(), s[..., None] * q.float())
+    assert int(pq[:4].abs().max()) == 0  # (where an offset cut to 32 bits would land)

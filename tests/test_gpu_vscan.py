@@ -395,3 +395,26 @@ def test_two_workspaces_at_once():
     y, _, ws2 = naju.vscan_fwd(t["h"], t["a"], t["b"], z=t["z"], x0=t["x0"], workspace=ws)
     g = naju.vscan_bwd(t["dy"], t["h"], t["a"], t["b"], ws, z=t["z"], dx_final=t["dx_final"])
     assert ws2 is ws and torch.equal(y, want[1][0]) and torch.equal(g["dh"], want[1][2]["dh"])
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last tokens equal their own run from the
+    state before them, and so do their gradients."""
+    L, d, cut = 1_049_000, 2048, 1_048_900
+    assert L * d > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rn = lambda: torch.randn(1, L, d, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    h, a = rn(), rn().add_(4.0)
+    y, xf, ws = naju.vscan_fwd(h, a)
+    assert naju.last_device_status(ws) == 0
+    tail = lambda t: t[:, cut:].contiguous()  # noqa: E731
+    before = naju.vscan_fwd(h[:, :cut].contiguous(), a[:, :cut].contiguous())[1]
+    y2, xf2, ws2 = naju.vscan_fwd(tail(h), tail(a), x0=before)
+    # a state of at most about one, summed in another order; bf16 results
+    assert float((xf - xf2).abs().max()) <= 1e-5
+    assert float((tail(y).float() - y2.float()).abs().max()) <= 2.0 ** -7 * float(y2.abs().max())
+    grads = naju.vscan_bwd(h, h, a, None, ws, want_dx0=False)
+    grads2 = naju.vscan_bwd(tail(h), tail(h), tail(a), None, ws2)
+    for n in ("dh", "da"):
+        one, two = tail(grads[n]).float(), grads2[n].float()
+        assert float((one - two).abs().max()) <= 2.0 ** -7 * float(two.abs().max()), n

@@ -286,3 +286,25 @@ def test_two_calls_at_once():
                 got.append(naju.w4_linear(t, wq, scales, 64))
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("m", [1, 9, 40])
+def test_offsets_past_32_bits(m):
+    """Weights of more than 2^31 bytes: the last rows equal a product with them
+    alone."""
+    K, O, tail = 16384, 263000, 129
+    g = torch.Generator(device="cuda").manual_seed(1)
+    wq = torch.randint(0, 256, (O, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    assert wq.numel() > 2 ** 31
+    scales = torch.rand(O, K // 128, generator=g, device="cuda").add_(0.5).bfloat16()
+    x = torch.randn(m, K, generator=g, device="cuda").bfloat16()
+    y = naju.w4_linear(x, wq, scales)
+    for impl in (0, 1, 2):
+        naju.testing_set_w4_impl(impl)
+        try:
+            last = naju.w4_linear(x, wq[-tail:].contiguous(), scales[-tail:].contiguous())
+        finally:
+            naju.testing_set_w4_impl(0)
+        # the order of the sums may differ: two roundings to bf16
+        err = (y[:, -tail:].double() - last.double()).abs()
+        assert bool((err <= 2.0 ** -7 * last.double().abs() + 1e-2).all())
