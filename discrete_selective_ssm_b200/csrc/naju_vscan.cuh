@@ -23,7 +23,8 @@
 // next item's tiles brought in by TMA as soon as the compute warps have read
 // the present one's.  Measured against items taken from a ticket with a
 // look-back through global flags (16 x 4096 x 2048 bf16 / 1 x 65536 x 2048):
-// forward 305 / 803 us there, see the launch functions for the figures here.
+// forward 305 / 803 us there, 256 / 352 us here; backward 1031 / 2231 and
+// 582 / 601 us.
 #pragma once
 #include "naju_common.cuh"
 #include "naju_kernels.h"
@@ -223,8 +224,13 @@ __device__ __forceinline__ void send_pair(uint32_t dst, const VPair<2>& v, uint3
         "r"(__float_as_uint(v.X.x.x)), "r"(__float_as_uint(v.X.x.y)), "r"(mbar)
         : "memory");
 }
+// All blocks of the cluster have come this far.  Relaxed: nothing but the
+// mbarriers' initialisation (fenced by itself) and the right to leave depends
+// on it, so a block does not wait for its stores here.
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    asm volatile(
+        "barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+            : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
