@@ -1,7 +1,8 @@
 """ctypes binding of libnaju.so (include/naju.h, include/naju_testing.h).
 
-Argument marshalling only: every function here checks tensor placement,
-dtype and contiguity, allocates outputs with torch on the inputs' device,
+Argument marshalling only: every function here (those of the vector-state scan,
+the 4-bit product and the state cache through the compiled _naju_bind module)
+checks tensor placement, dtype and contiguity, allocates outputs with torch on the inputs' device,
 passes raw device pointers and the current CUDA stream to the C ABI, and
 raises NajuError on a non-OK status.  All arithmetic runs in the library's
 CUDA kernels; there is no host or PyTorch fallback.
@@ -9,6 +10,8 @@ CUDA kernels; there is no host or PyTorch fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
 import threading
@@ -112,6 +115,29 @@ def lib(build_if_missing: bool = True):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
+
+
+_bind = None
+
+
+def _load_bind():
+    """The compiled marshalling module, bound to the loaded library.  Raises if
+    it cannot be had (there is no other path for its functions)."""
+    global _bind
+    L = lib()
+    with _lock:
+        if _bind is None:
+            path = _build.BIND if os.path.exists(_build.BIND) else _build.build_bind()
+            loader = importlib.machinery.ExtensionFileLoader("_naju_bind", path)
+            spec = importlib.util.spec_from_file_location("_naju_bind", path, loader=loader)
+            mod = importlib.util.module_from_spec(spec)
+            loader.exec_module(mod)
+            addr = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+            mod.bind(NajuError, addr(L.naju_vscan_workspace_bytes), addr(L.naju_vscan_fwd),
+                     addr(L.naju_vscan_bwd), addr(L.naju_vscan_step), addr(L.naju_w4_linear),
+                     addr(L.naju_state_store), addr(L.naju_state_load))
+            _bind = mod
+    return _bind
 
 
 def declared_symbols() -> list[str]:
@@ -318,70 +344,15 @@ def scan_step_conv(state, conv_state, u, a, b, B, C, conv_w, conv_b=None, z=None
 
 
 # ------------------------------------------------------- vector-state scan
-_C = torch._C
-
-
-def _arg(t, name: str, shape, dtype, device):
-    """Data pointer of an argument that must be a contiguous `dtype` tensor of
-    `shape` on the CUDA device number `device` (None passes through)."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
-        return t.data_ptr()
-    if t.get_device() != device or device < 0:
-        raise ValueError(f"{name} must be a CUDA tensor on device {device}, got {t.device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _cuda_index(t, name: str) -> int:
-    i = t.get_device()
-    if i < 0:
-        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
-    return i
-
-
-def _launch(fn, device: int, stream, *args):
-    """fn(*args, raw stream) with CUDA device number `device` current; `stream`
-    defaults to that device's current one."""
-    raw = _C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-    if _C._cuda_getDevice() == device:
-        st = fn(*args, raw)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, raw)
-    if st:
-        raise NajuError(st, fn.__name__)
-
-
-def _vdims(h, out_dtype) -> Dims:
-    if h.dim() != 3:
-        raise ValueError(f"h must be [batch, seqlen, d_inner], got {tuple(h.shape)}")
-    dt = _dt(h)
-    return Dims(*h.shape, 1, 0, dt, dt if out_dtype is None else out_dtype, 0)
-
-
 def vscan_workspace(dims: Dims, like: torch.Tensor) -> torch.Tensor:
     """A workspace of vscan_fwd and vscan_bwd on the device of `like`
-    (contents undefined)."""
+    (contents undefined); dims as make_dims(batch, seqlen, d_inner, 1, ...)."""
     n = lib().naju_vscan_workspace_bytes(ctypes.byref(dims))
     if n == 0:
         raise NajuError(1, "naju_vscan_workspace_bytes")
-    ws = like.new_empty(n, dtype=torch.uint8)
-    if ws.data_ptr() % 256:  # (an allocator that aligns less than CUDA's)
-        ws = like.new_empty(n + 256, dtype=torch.uint8)
-        off = (-ws.data_ptr()) % 256
-        ws = ws[off:off + n]
-    return ws
-
-
-def _ws_arg(ws, device: int):
-    if ws.dtype is not torch.uint8 or ws.get_device() != device or not ws.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on CUDA device {device}")
-    return ws.data_ptr()
+    ws = like.new_empty(n + 256, dtype=torch.uint8)
+    off = (-ws.data_ptr()) % 256
+    return ws[off:off + n]
 
 
 def vscan_fwd(h, a, b=None, *, z=None, x0=None, out_dtype=None, workspace=None, want_final=True,
@@ -389,21 +360,8 @@ def vscan_fwd(h, a, b=None, *, z=None, x0=None, out_dtype=None, workspace=None, 
     """Vector-state scan over [batch, seqlen, d_inner]: x_t = f x_{t-1} + i h,
     y = x SiLU(z).  b None: coupled gate; z None: no modulation.  Returns
     (y, x_final, workspace); the workspace is what vscan_bwd needs."""
-    dims = _vdims(h, out_dtype)
-    dev, dt, act, f32 = _cuda_index(h, "h"), h.dtype, h.shape, torch.float32
-    st, ot = (act[0], act[2]), _torch_dt(dims.out_dtype)
-    L = _lib or lib()
-    if workspace is None:
-        workspace = vscan_workspace(dims, h)
-    if y is None:
-        y = torch.empty_like(h, dtype=ot)
-    if x_final is None and want_final:
-        x_final = h.new_empty(st, dtype=f32)
-    _launch(L.naju_vscan_fwd, dev, stream, ctypes.byref(dims), _arg(h, "h", act, dt, dev),
-            _arg(a, "a", act, dt, dev), _arg(b, "b", act, dt, dev), _arg(z, "z", act, dt, dev),
-            _arg(x0, "x0", st, f32, dev), _arg(y, "y", act, ot, dev),
-            _arg(x_final, "x_final", st, f32, dev), _ws_arg(workspace, dev), workspace.numel())
-    return y, x_final, workspace
+    return (_bind or _load_bind()).vscan_fwd(h, a, b, z, x0, out_dtype, workspace, want_final, y,
+                                             x_final, stream)
 
 
 def vscan_bwd(dy, h, a, b, workspace, *, z=None, dx_final=None, out_dtype=None, want_dx0=True,
@@ -411,47 +369,17 @@ def vscan_bwd(dy, h, a, b, workspace, *, z=None, dx_final=None, out_dtype=None, 
     """Gradients of vscan_fwd; `workspace` must hold that forward's
     checkpoints.  Returns a dict: dh, da, db (None without b), dz (None
     without z), dx0 (None unless wanted)."""
-    dims = _vdims(h, out_dtype)
-    dev, dt, act, f32 = _cuda_index(h, "h"), h.dtype, h.shape, torch.float32
-    st, ot = (act[0], act[2]), _torch_dt(dims.out_dtype)
-    L = _lib or lib()
-    if grads is None:
-        grads = {"dh": torch.empty_like(h, dtype=ot), "da": torch.empty_like(h, dtype=ot),
-                 "db": None if b is None else torch.empty_like(h, dtype=ot),
-                 "dz": None if z is None else torch.empty_like(h, dtype=ot),
-                 "dx0": h.new_empty(st, dtype=f32) if want_dx0 else None}
-    g = grads
-    _launch(L.naju_vscan_bwd, dev, stream, ctypes.byref(dims), _arg(h, "h", act, dt, dev),
-            _arg(a, "a", act, dt, dev), _arg(b, "b", act, dt, dev), _arg(z, "z", act, dt, dev),
-            _arg(dy, "dy", act, dt, dev), _arg(dx_final, "dx_final", st, f32, dev),
-            _arg(g["dh"], "dh", act, ot, dev), _arg(g["da"], "da", act, ot, dev),
-            _arg(g.get("db"), "db", act, ot, dev), _arg(g.get("dz"), "dz", act, ot, dev),
-            _arg(g.get("dx0"), "dx0", st, f32, dev), _ws_arg(workspace, dev), workspace.numel())
-    return g
+    return (_bind or _load_bind()).vscan_bwd(dy, h, a, b, workspace, z, dx_final, out_dtype,
+                                             want_dx0, grads, stream)
 
 
 def vscan_step(state, h, a, b=None, z=None, y=None, stream=None):
     """One decode step of the vector-state scan: h, a, b, z [batch, d_inner];
     `state` [batch, d_inner] fp32 is updated in place.  Returns y."""
-    sh = h.shape
-    if len(sh) != 2:
-        raise ValueError(f"h must be [batch, d_inner], got {tuple(sh)}")
-    dev, dt, code = _cuda_index(h, "h"), h.dtype, _dt(h)
-    L = _lib or lib()
-    if y is None:
-        y = torch.empty_like(h)
-    _launch(L.naju_vscan_step, dev, stream, sh[0], sh[1], code, _arg(h, "h", sh, dt, dev),
-            _arg(a, "a", sh, dt, dev), _arg(b, "b", sh, dt, dev), _arg(z, "z", sh, dt, dev),
-            _arg(state, "state", sh, torch.float32, dev), _arg(y, "y", sh, dt, dev))
-    return y
+    return (_bind or _load_bind()).vscan_step(state, h, a, b, z, y, stream)
 
 
 # ------------------------------------------------------ 4-bit projections
-def _w4_group(group: int):
-    if group not in (32, 64, 128):
-        raise NajuError(2, f"4-bit projection with groups of {group}")
-
-
 def w4_quantize(W, group=128, stream=None):
     """Quantises a projection W [n_out, n_in] to 4 bits a weight with one bf16
     scale per `group` (32, 64 or 128) inputs.  Returns (wq, scales): uint8
@@ -459,13 +387,15 @@ def w4_quantize(W, group=128, stream=None):
     [n_out, ceil(n_in / group)]."""
     if W.dim() != 2:
         raise ValueError(f"W must be [n_out, n_in], got {tuple(W.shape)}")
-    _w4_group(group)
-    dev, (O, K), code = _cuda_index(W, "W"), W.shape, _dt(W)
-    L = _lib or lib()
-    wq = torch.empty((O, -(-K // 128) * 64), dtype=torch.uint8, device=W.device)
-    scales = torch.empty((O, -(-K // group)), dtype=torch.bfloat16, device=W.device)
-    _launch(L.naju_w4_quantize, dev, stream, O, K, group, code,
-            _arg(W, "W", W.shape, W.dtype, dev), wq.data_ptr(), scales.data_ptr())
+    if group not in (32, 64, 128):
+        raise NajuError(2, f"4-bit projection with groups of {group}")
+    O, K = W.shape
+    args = (O, K, group, _dt(W), _ptr(W, "W"))
+    with torch.cuda.device(W.device):
+        wq = torch.empty((O, -(-K // 128) * 64), dtype=torch.uint8, device=W.device)
+        scales = torch.empty((O, -(-K // group)), dtype=torch.bfloat16, device=W.device)
+        _check(lib().naju_w4_quantize(*args, _ptr(wq, "wq"), _ptr(scales, "scales"),
+                                      _stream(stream)), "naju_w4_quantize")
     return wq, scales
 
 
@@ -473,19 +403,7 @@ def w4_linear(x, wq, scales, group=128, bias=None, residual=None, y=None, stream
     """y = x W^T (+ bias) (+ residual) with the 4-bit W of w4_quantize:
     x [..., n_in] (its leading dimensions are rows), bias [n_out] fp32, residual
     and y [..., n_out] in x's dtype."""
-    _w4_group(group)
-    sh, O = x.shape, wq.shape[0]
-    dev, dt, K, code = _cuda_index(x, "x"), x.dtype, sh[-1], _dt(x)
-    out = (*sh[:-1], O)
-    L = _lib or lib()
-    if y is None:
-        y = x.new_empty(out)
-    _launch(L.naju_w4_linear, dev, stream, x.numel() // K if K else 0, K, O, group, code,
-            _arg(x, "x", sh, dt, dev), _arg(wq, "wq", (O, -(-K // 128) * 64), torch.uint8, dev),
-            _arg(scales, "scales", (O, -(-K // group)), torch.bfloat16, dev),
-            _arg(bias, "bias", (O,), torch.float32, dev),
-            _arg(residual, "residual", out, dt, dev), _arg(y, "y", out, dt, dev))
-    return y
+    return (_bind or _load_bind()).w4_linear(x, wq, scales, group, bias, residual, y, stream)
 
 
 # -------------------------------------------------------- 8-bit state cache
@@ -496,38 +414,18 @@ def state_pool(n_slots: int, d_inner: int, d_state: int, device):
             torch.zeros((n_slots, d_inner), dtype=torch.float32, device=device))
 
 
-def _cache_args(pool_q, pool_scale, slots):
-    sh = pool_q.shape
-    if len(sh) != 3:
-        raise ValueError(f"pool_q must be [n_slots, d_inner, d_state], got {tuple(sh)}")
-    if slots.dim() != 1:
-        raise ValueError(f"slots must be [n], got {tuple(slots.shape)}")
-    dev = _cuda_index(pool_q, "pool_q")
-    n = slots.shape[0]
-    return (dev, (n, sh[1], sh[2], sh[0]), _arg(pool_q, "pool_q", sh, torch.int8, dev),
-            _arg(pool_scale, "pool_scale", sh[:2], torch.float32, dev),
-            _arg(slots, "slots", (n,), torch.int32, dev))
-
-
 def state_store(state, slots, pool_q, pool_scale, stream=None):
     """Parks decode states: batch place i of `state` [n, d_inner, d_state] fp32
     into slot slots[i] (int32) of the pool, 8 bits a value with one scale per
     row.  Slots outside the pool store nothing; of places that name the same
     slot the last is stored."""
-    dev, sizes, q, sc, sl = _cache_args(pool_q, pool_scale, slots)
-    _launch((_lib or lib()).naju_state_store, dev, stream, *sizes,
-            _arg(state, "state", sizes[:3], torch.float32, dev), sl, q, sc)
+    (_bind or _load_bind()).state_store(state, slots, pool_q, pool_scale, stream)
 
 
 def state_load(pool_q, pool_scale, slots, state=None, stream=None):
     """Resumes parked states: slot slots[i] into batch place i.  Slots outside
     the pool give a zero state.  Returns state [n, d_inner, d_state] fp32."""
-    dev, sizes, q, sc, sl = _cache_args(pool_q, pool_scale, slots)
-    if state is None:
-        state = pool_scale.new_empty(sizes[:3])
-    _launch((_lib or lib()).naju_state_load, dev, stream, *sizes, q, sc, sl,
-            _arg(state, "state", sizes[:3], torch.float32, dev))
-    return state
+    return (_bind or _load_bind()).state_load(pool_q, pool_scale, slots, state, stream)
 
 
 def last_device_status(workspace, stream=None) -> int:

@@ -6,22 +6,27 @@ nvcc compiles every ``csrc/*.cu`` to an object file (in parallel, under
 ``_build/`` at the repository root) and links them into one shared library
 next to this file; the build is skipped when the library is newer than all
 sources and headers, and an object is recompiled only when it is older than
-its source or any header.
+its source or any header.  g++ compiles ``csrc/naju_bind.cpp``, the compiled
+part of the Python binding, against the installed torch.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libnaju.so")
+BIND = os.path.join(HERE, "_naju_bind.so")
+BIND_SRC = os.path.join(CSRC, "naju_bind.cpp")
 OBJDIR = os.path.join(ROOT, "_build")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -70,7 +75,30 @@ def _compile(src: str, force: bool, verbose: bool) -> str:
     return obj
 
 
+def build_bind(force: bool = False, verbose: bool = False) -> str:
+    """The compiled part of the Python binding (an extension module)."""
+    deps = [BIND_SRC, os.path.join(INCLUDE, "naju.h")]
+    if not force and os.path.exists(BIND) and all(
+            os.path.getmtime(f) <= os.path.getmtime(BIND) for f in deps):
+        return BIND
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           "-I", os.path.join(torch, "include"),
+           "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-o", tmp, BIND_SRC, "-L", os.path.join(torch, "lib"), "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_bind(force, verbose)
     if not force and not _stale():
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)
