@@ -291,20 +291,21 @@ __global__ void __launch_bounds__(256) w4_linear_kernel(const W4Params p) {
         cl.sync();
     else
         __syncthreads();
-    for (int e = rank * 256 + tid; e < ROWS * COLS; e += 256 * p.split) {
-        const int row = e % ROWS, col = e / ROWS;
+    // four rows of W at a time (an access to another block takes as long as a
+    // dozen of these sums)
+#pragma unroll 2
+    for (int e = rank * 256 + tid; e < ROWS * COLS / 4; e += 256 * p.split) {
+        const int row = e % (ROWS / 4) * 4, col = e / (ROWS / 4);
         const int64_t o = row0 + row, m = col0 + col;
         if (o >= p.n_out || m >= p.m) continue;
-        float v = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int s = 0; s < p.split; ++s) {
             const float* from = p.split > 1 ? cl.map_shared_rank(red, s) : red;
 #pragma unroll
-            for (int k = 0; k < WK; ++k) v += from[(k * COLS + col) * ROWS + row];
+            for (int k = 0; k < WK; ++k)
+                v = v + *reinterpret_cast<const float4*>(from + (k * COLS + col) * ROWS + row);
         }
-        v *= 1024.f;
-        if (p.bias) v += p.bias[o];
-        if (p.residual) v += to_f(static_cast<const T*>(p.residual)[m * p.n_out + o]);
-        static_cast<T*>(p.y)[m * p.n_out + o] = from_f<T>(v);
+        w4_finish<T>(p, m, o, v);
     }
     if (p.split > 1) cl.sync();  // no block leaves while another reads from it
 }

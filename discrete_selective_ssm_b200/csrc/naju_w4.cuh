@@ -49,6 +49,45 @@ __device__ __forceinline__ uint32_t unpack_pair(uint32_t w, int i, const PairBit
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// Finishes four sums of one row of x (outputs o .. o + 3): the factor, bias and
+// residual, one rounding.
+template <typename T>
+__device__ __forceinline__ void w4_finish(const W4Params& p, int64_t m, int64_t o, float4 s) {
+    float v[4] = {s.x * 1024.f, s.y * 1024.f, s.z * 1024.f, s.w * 1024.f};
+    const int n = (int)min64(4, p.n_out - o);
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) v[i] += p.bias[o + i];
+    }
+    const T* res = static_cast<const T*>(p.residual);
+    T* y = static_cast<T*>(p.y) + m * p.n_out + o;
+    if (p.n_out % 4 == 0) {  // rows start on four elements
+        struct alignas(4 * sizeof(T)) Four {
+            T e[4];
+        } r;
+        if (res) {
+            r = *reinterpret_cast<const Four*>(res + m * p.n_out + o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += to_f(r.e[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.e[i] = from_f<T>(v[i]);
+        *reinterpret_cast<Four*>(y) = r;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i < n) {
+                if (res) v[i] += to_f(res[m * p.n_out + o + i]);
+                y[i] = from_f<T>(v[i]);
+            }
+        }
+    }
+}
+__device__ __forceinline__ float4 operator+(float4 a, float4 b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
 // Launches clusters of `split` blocks.  `ready`: the devices on which this
 // kernel's attributes are set.
 template <typename... Args>

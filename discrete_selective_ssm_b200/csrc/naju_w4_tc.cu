@@ -262,18 +262,19 @@ w4_tc_kernel(const __grid_constant__ W4Params p, const __grid_constant__ CUtenso
         tmem_dealloc(tm, C::kCols);
     }
     const float* red = reinterpret_cast<const float*>(ring);
-    for (int e = rank * kTcThreads + tid; e < N * 128; e += kTcThreads * p.split) {
-        const int64_t o = row0 + e % 128, m = col0 + e / 128;
+    bool bad = s_bad;
+    for (int s = 0; p.split > 1 && s < p.split; ++s) bad |= *cl.map_shared_rank(&s_bad, s) != 0;
+#pragma unroll 2
+    for (int e = rank * kTcThreads + tid; e < N * 32; e += kTcThreads * p.split) {
+        const int64_t o = row0 + e % 32 * 4, m = col0 + e / 32;
         if (o >= p.n_out || m >= p.m) continue;
-        float v = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int s = 0; s < p.split; ++s) {  // in fixed order
-            v += p.split > 1 ? cl.map_shared_rank(red, s)[e] : red[e];
-            if (p.split > 1 ? *cl.map_shared_rank(&s_bad, s) : s_bad) v = NAN;
+            const float* from = p.split > 1 ? cl.map_shared_rank(red, s) : red;
+            v = v + reinterpret_cast<const float4*>(from)[e];
         }
-        v *= 1024.f;
-        if (p.bias) v += p.bias[o];
-        if (p.residual) v += to_f(static_cast<const bf*>(p.residual)[m * p.n_out + o]);
-        static_cast<bf*>(p.y)[m * p.n_out + o] = from_f<bf>(v);
+        if (bad) v = make_float4(NAN, NAN, NAN, NAN);
+        w4_finish<bf>(p, m, o, v);
     }
     if (p.split > 1) cl.sync();  // no block leaves while another reads from it
 }
