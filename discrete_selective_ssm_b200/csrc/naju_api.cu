@@ -278,12 +278,21 @@ VLayout vlayout(const naju_dims* dm) {
 // 134, 120, 131; 32 units of 65536 tokens 1630, 951, 482, 353 / 3078, 1619,
 // 901, 601 (twelve to sixteen blocks: 398 and more / 758 and more, those
 // clusters fill the GPU's processor groups unevenly); one unit of 65536
-// tokens 250 at eight, 143 at sixteen.
+// tokens 250 at eight, 143 at sixteen; 16 units of 16384 tokens 88 / 139 at
+// eight, 66 / 101 at twelve, 64 / 136 at sixteen; 20 units 88 / 141, 66 / 105,
+// 65 / 137; 24 units 88 / 143, 86 / 175, 90 / 154.
 int vscan_cluster(int64_t units, int64_t nk, int slots) {
     if (g_vcluster > 0) return g_vcluster;
     int cs = 1;
     while (cs < 8 && cs < nk && 2 * units * cs < 3LL * slots) cs *= 2;
-    if (cs == 8 && nk > 8 && units * 16 <= slots) cs = 16;
+    // larger clusters than the portable eight fill the processor groups unevenly:
+    // they have to fit with some places to spare
+    if (cs == 8 && nk > 8) {
+        if (units * 64 <= 3LL * slots)
+            cs = 16;
+        else if (units * 72 <= 5LL * slots)
+            cs = 12;
+    }
     return cs;
 }
 
