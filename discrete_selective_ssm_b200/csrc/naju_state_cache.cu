@@ -1,7 +1,7 @@
 // 8-bit cache of decode states: store (quantise into pool slots) and load
 // (dequantise into batch places).  sm_100a, memory-bound.
 //
-// A row of N state values has scale = fp32(max|x| / 127) and
+// A row of N state values has scale = max|x| (1 / 127), a product in fp32, and
 // q = round(x / scale), the exact quotient rounded to nearest, ties to even.
 // A warp takes 32 / Q whole rows per instruction, Q = N / 4 lanes a row, four
 // values (16 bytes of fp32, 4 bytes of int8) a lane, and kBatch such
@@ -75,7 +75,7 @@ state_store_kernel(int64_t n, int64_t d, int64_t n_slots, const float* __restric
         for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(e[i]) & 0x7fffffffu);
 #pragma unroll
         for (int o = 1; o < Q; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float s = m < 0x7f800000u ? __fdiv_rn(__uint_as_float(m), 127.f) : NAN;
+        const float s = m < 0x7f800000u ? __uint_as_float(m) * (1.f / 127.f) : NAN;
         uint32_t q = 0;
         if (s > 0.f) {
             const float inv = rcpa_(s);

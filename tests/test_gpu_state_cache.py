@@ -12,10 +12,10 @@ pytestmark = pytest.mark.gpu
 
 
 def reference(x):
-    """q and scale of rows (last axis) in 64 bits; scale rounded to fp32."""
-    x = x.double().cpu()
-    scale = (x.abs().amax(-1) / 127).float()
-    s = scale.double()
+    """q and scale of rows (last axis): the scale as the format defines it (one
+    fp32 product, equal on both sides), the quotients in 64 bits."""
+    scale = x.float().cpu().abs().amax(-1) * torch.tensor(1.0 / 127.0, dtype=torch.float32)
+    x, s = x.double().cpu(), scale.double()
     q = torch.round(x / torch.where(s > 0, s, 1.0)[..., None])
     q[s == 0] = 0
     return q.clamp(-127, 127).to(torch.int8), scale
