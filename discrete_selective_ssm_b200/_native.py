@@ -108,10 +108,12 @@ def lib(build_if_missing: bool = True):
             L.naju_state_load.argtypes = [i64] * 4 + [vp] * 5
             L.naju_w4_quantize.argtypes = [i64] * 2 + [i32] * 2 + [vp] * 4
             L.naju_w4_linear.argtypes = [i64] * 3 + [i32] * 2 + [vp] * 7
-            for name in ("naju_w4_quantize", "naju_w4_linear", "naju_state_store", "naju_state_load", "naju_vscan_fwd", "naju_vscan_bwd", "naju_vscan_step",
-                         "naju_conv_silu_fwd", "naju_conv_silu_bwd", "naju_scan_fwd",
-                         "naju_scan_bwd", "naju_scan_step", "naju_conv_silu_step",
-                         "naju_scan_step_conv", "naju_last_device_status"):
+            for name in ("naju_w4_quantize", "naju_w4_linear", "naju_state_store",
+                         "naju_state_load", "naju_vscan_fwd", "naju_vscan_bwd",
+                         "naju_vscan_step", "naju_conv_silu_fwd", "naju_conv_silu_bwd",
+                         "naju_scan_fwd", "naju_scan_bwd", "naju_scan_step",
+                         "naju_conv_silu_step", "naju_scan_step_conv",
+                         "naju_last_device_status"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib

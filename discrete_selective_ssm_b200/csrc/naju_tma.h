@@ -36,13 +36,6 @@ bool tma_encode_bf16_3d_sw128(CUtensorMap* map, const void* base, int64_t outer,
 bool tma_encode_f32_3d_sw128(CUtensorMap* map, const void* base, int64_t outer, int64_t rows,
                              int64_t cols, int box_rows);
 
-// Encode a map over rows of 2-byte elements whose box is box_rows rows of 32
-// elements (64 bytes; as 3-D with one outer element), written in the 64-byte
-// swizzled layout: box row r at byte 64 r, its 16-byte chunks XOR-permuted by
-// (r / 2) % 4 (destination 512-byte aligned).  Same checks.
-bool tma_encode_2b_2d_sw64(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
-                           int box_rows);
-
 #ifdef __CUDACC__
 namespace tma {
 

@@ -38,7 +38,7 @@ __device__ __forceinline__ uint32_t held(uint32_t v) {
 // factor keeps a group's sum (at most 128 * 8 values of x) in range for every
 // finite x; the sums are multiplied by 1024 once, at the end.
 struct PairBits {
-    uint32_t mask = 0x000f000fu, bits = 0x43004300u;
+    uint32_t mask, bits;
     __device__ __forceinline__ PairBits() : mask(held(0x000f000fu)), bits(held(0x43004300u)) {}
 };
 __device__ __forceinline__ uint32_t unpack_pair(uint32_t w, int i, const PairBits& k) {

@@ -240,7 +240,8 @@ naju_status naju_w4_quantize(int64_t n_out, int64_t n_in, int32_t group, int32_t
  * y itself, x may not (INVALID_ARG).  Sums are fp32 and every product is exact (bf16 x) or exact to
  * 2^-24 of it (fp32 x); y is rounded once.  m is at most 2^20, but the
  * weights are read again for every 64 rows of x: meant for m up to a few
- * hundred.  Uses no workspace. */
+ * hundred.  Uses no workspace; a bounded wait inside that runs out shows as
+ * NaN in the outputs. */
 naju_status naju_w4_linear(int64_t m, int64_t n_in, int64_t n_out, int32_t group, int32_t dtype,
                            const void* x, const void* wq, const void* scales, const float* bias,
                            const void* residual, void* y, void* stream);
