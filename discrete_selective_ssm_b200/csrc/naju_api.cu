@@ -269,28 +269,29 @@ VLayout vlayout(const naju_dims* dm) {
     return l;
 }
 
-// Blocks per unit of the vector-state scan: enough for one and a half times
-// the blocks that run at once (`slots`), so that the last wave is short, and
-// no more, since every exchange grows with them; more than the portable eight
-// only where all units together are still few.  Measured (bf16, forward /
+// Blocks per unit of the vector-state scan: enough for four blocks per SM (of
+// which `resident`, three forward and two backward, run at once), so that the
+// last wave is short, and no more, since every exchange grows with them; more
+// than the portable eight only where all units together are still few.  Measured (bf16, forward /
 // backward us at 1, 2, 4, 8 blocks): 512 units of 4096 tokens 285, 256, 277,
-// 322 / 582, 572, 583, 620; 192 units of 2048 tokens 80, 62, 65, 73 / 138,
+// 322 / 582, 565, 571, 620; 192 units of 2048 tokens 80, 62, 65, 73 / 138,
 // 134, 120, 131; 32 units of 65536 tokens 1630, 951, 482, 353 / 3078, 1619,
 // 901, 601 (twelve to sixteen blocks: 398 and more / 758 and more, those
 // clusters fill the GPU's processor groups unevenly); one unit of 65536
 // tokens 250 at eight, 143 at sixteen; 16 units of 16384 tokens 88 / 139 at
 // eight, 66 / 101 at twelve, 64 / 136 at sixteen; 20 units 88 / 141, 66 / 105,
 // 65 / 137; 24 units 88 / 143, 86 / 175, 90 / 154.
-int vscan_cluster(int64_t units, int64_t nk, int slots) {
+int vscan_cluster(int64_t units, int64_t nk, int resident) {
     if (g_vcluster > 0) return g_vcluster;
+    const int64_t sms = sm_count(), slots = resident * sms;
     int cs = 1;
-    while (cs < 8 && cs < nk && 2 * units * cs < 3LL * slots) cs *= 2;
+    while (cs < 8 && cs < nk && units * cs < 4 * sms) cs *= 2;
     // larger clusters than the portable eight fill the processor groups unevenly:
     // they have to fit with some places to spare
     if (cs == 8 && nk > 8) {
-        if (units * 64 <= 3LL * slots)
+        if (units * 64 <= 3 * slots)
             cs = 16;
-        else if (units * 72 <= 5LL * slots)
+        else if (units * 72 <= 5 * slots)
             cs = 12;
     }
     return cs;
@@ -553,7 +554,7 @@ naju_status naju_vscan_fwd(const naju_dims* dims, const void* h, const void* a, 
     vscan_params(p, dims, l, ws);
     p.h = h; p.a = a; p.b = b; p.z = z; p.x0 = x0; p.y = y; p.x_final = x_final;
     p.nk = l.nkf;
-    p.cluster = vscan_cluster(l.units, l.nkf, 3 * sm_count());
+    p.cluster = vscan_cluster(l.units, l.nkf, 3);
     return cuda_status(launch_vscan_fwd(p, dims->dtype, dims->out_dtype, s));
 }
 
@@ -576,7 +577,7 @@ naju_status naju_vscan_bwd(const naju_dims* dims, const void* h, const void* a, 
     p.h = h; p.a = a; p.b = b; p.z = z; p.dy = dy; p.dx_final = dx_final;
     p.dh = dh; p.da = da; p.db = db; p.dz = dz; p.dx0 = dx0;
     p.nk = l.nkb;
-    p.cluster = vscan_cluster(l.units, l.nkb, 2 * sm_count());
+    p.cluster = vscan_cluster(l.units, l.nkb, 2);
     return cuda_status(launch_vscan_bwd(p, dims->dtype, dims->out_dtype, s));
 }
 

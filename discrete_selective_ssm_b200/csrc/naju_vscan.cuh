@@ -24,7 +24,7 @@
 // the present one's.  Measured against items taken from a ticket with a
 // look-back through global flags (16 x 4096 x 2048 bf16 / 1 x 65536 x 2048):
 // forward 305 / 803 us there, 252 / 351 us here (5.3 and 3.8 TB/s); backward
-// 1031 / 2231 and 582 / 598 us (4.2 and 4.0 TB/s).
+// 1031 / 2231 and 570 / 600 us (4.2 and 4.0 TB/s).
 #pragma once
 #include "naju_common.cuh"
 #include "naju_kernels.h"
