@@ -1,8 +1,9 @@
 // 8-bit cache of decode states: store (quantise into pool slots) and load
 // (dequantise into batch places).  sm_100a, memory-bound.
 //
-// A row of N state values has scale = max|x| (1 / 127), a product in fp32, and
-// q = round(x / scale), the exact quotient rounded to nearest, ties to even.
+// A row of N state values has scale = fp32(max|x| / 127) and
+// q = round(x / scale), both quotients exact before their one rounding (to
+// nearest, ties to even).
 // A warp takes 32 / Q whole rows per instruction, Q = N / 4 lanes a row, four
 // values (16 bytes of fp32, 4 bytes of int8) a lane, and kBatch such
 // instructions in flight, so every access covers whole contiguous rows.
@@ -27,6 +28,15 @@ constexpr int kCacheThreads = 256;
 // about s), so comparing it with s / 2 settles the last step.  (The conversion
 // instructions run at an eighth of the adder's rate; the sum above costs none.)
 constexpr float kMagic = 12582912.f;  // 1.5 2^23
+
+// m / 127 rounded to fp32, for every finite m >= 0: the remainder m - 127 p of
+// the product p = m fp32(1 / 127) is exact, and what it adds to p is rounded once
+// (equal to the quotient for all 2^31 - 2^23 such m; the product alone is one
+// place off for one in 22).
+__device__ __forceinline__ float over_127(float m) {
+    const float p = m * (1.f / 127.f);
+    return fmaf(fmaf(-127.f, p, m), 1.f / 127.f, p);
+}
 
 __device__ __noinline__ int quant_exact(float x, float s) {
     // below the normal range both sides are scaled up by 2^24, exactly
@@ -77,7 +87,7 @@ state_store_kernel(int64_t n, int64_t d, int64_t n_slots, const float* __restric
         for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(e[i]) & 0x7fffffffu);
 #pragma unroll
         for (int o = 1; o < Q; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float s = m < 0x7f800000u ? __uint_as_float(m) * (1.f / 127.f) : NAN;
+        const float s = m < 0x7f800000u ? over_127(__uint_as_float(m)) : NAN;
         uint32_t q = 0;
         if (s > 0.f) {
             const float inv = rcpa_(s);

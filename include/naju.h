@@ -250,10 +250,10 @@ naju_status naju_w4_linear(int64_t m, int64_t n_in, int64_t n_out, int32_t group
  * of slots, a quarter of the fp32 state's size, and resumed in any batch
  * place.  pool_q [n_slots, d_inner, d_state] int8, pool_scale [n_slots,
  * d_inner] fp32; a row of d_state (16, 32, 64 or 128) values has
- * scale = max|x| * (1.0f / 127.0f), one fp32 product, and q = the exact
- * quotient x / scale rounded to nearest, ties to even (at most 127 in size,
- * where a scale below the normal range is itself coarse); it reads back as
- * scale * q.  A row with an infinity or a NaN reads back as NaN throughout. */
+ * scale = fp32(max|x| / 127) and q = the exact quotient x / scale rounded to
+ * nearest, ties to even (at most 127 in size, where a scale below the normal
+ * range is itself coarse); it reads back as scale * q.  A row with an
+ * infinity or a NaN reads back as NaN throughout. */
 
 /* Stores state [n, d_inner, d_state] fp32: batch place i into slot slots[i]
  * (device int32 [n]).  A slot outside [0, n_slots) stores nothing; where a

@@ -12,10 +12,10 @@ pytestmark = pytest.mark.gpu
 
 
 def reference(x):
-    """q and scale of rows (last axis): the scale as the format defines it (one
-    fp32 product, equal on both sides), the quotients in 64 bits."""
-    scale = x.float().cpu().abs().amax(-1) * torch.tensor(1.0 / 127.0, dtype=torch.float32)
-    x, s = x.double().cpu(), scale.double()
+    """q and scale of rows (last axis) in 64 bits; scale rounded to fp32."""
+    x = x.double().cpu()
+    scale = (x.abs().amax(-1) / 127).float()
+    s = scale.double()
     q = torch.round(x / torch.where(s > 0, s, 1.0)[..., None])
     q[s == 0] = 0
     return q.clamp(-127, 127).to(torch.int8), scale
@@ -171,3 +171,25 @@ def test_offsets_past_32_bits():
     assert torch.equal(pq[slots.long()].cpu(), q) and torch.equal(ps[slots.long()].cpu(), s)
     assert torch.equal(naju.state_load(pq, ps, slots).cpu(), s[..., None] * q.float())
     assert int(pq[:4].abs().max()) == 0  # (where an offset cut to 32 bits would land)
+
+
+def test_scale_is_the_rounded_quotient():
+    """Maxima of every size, subnormal ones among them, and the largest values'
+    neighbours: the stored scale is max / 127, rounded once."""
+    n, d, N = 4, 65536, 16
+    g = torch.Generator().manual_seed(17)
+    bits = torch.randint(0, 0x7f800000, (n, d), generator=g, dtype=torch.int64).int()
+    bits[0, :4096] = torch.arange(4096, dtype=torch.int32)               # the smallest
+    bits[1, :4096] = 0x7f7fffff - torch.arange(4096, dtype=torch.int32)  # the largest
+    bits[2, :] = 0x3f800000 + torch.randint(0, 1 << 23, (d,), generator=g, dtype=torch.int64).int()
+    top = bits.view(torch.float32)
+    x = torch.zeros(n, d, N)
+    x[..., 5] = -top
+    x[..., 9] = top / 3
+    pq, ps = naju.state_pool(n, d, N, "cuda")
+    naju.state_store(x.cuda(), torch.arange(n, dtype=torch.int32, device="cuda"), pq, ps)
+    q, s = reference(x)
+    want = torch.from_numpy(top.numpy() / np.float32(127))  # IEEE division
+    assert torch.equal(s, want) and torch.equal(ps.cpu(), want)
+    fine = want >= 2.0 ** -126  # (a scale below the normal range is itself coarse)
+    assert torch.equal(pq.cpu()[fine], q[fine])
