@@ -96,10 +96,12 @@ template <> struct VRow<__nv_bfloat16> {
 // --------------------------------------------------------------- the gates
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Both sides of sigmoid(a), each to full relative accuracy and without
-// overflow: with t = e^{-|a|} <= 1 and r = 1 / (1 + t), the larger of
-// sigmoid(a) and 1 - sigmoid(a) is r and the smaller s = t r.  A NaN logit
-// makes both NaN.
+// Both sides of sigmoid(a) without overflow: with t = e^{-|a|} <= 1 and r =
+// 1 / (1 + t), the larger of sigmoid(a) and 1 - sigmoid(a) is r and the smaller
+// s = t r.  s is off by about |a| + 6 roundings of itself (the argument's own
+// in a base-2 exponential, its two steps, sum, reciprocal, product) and zero
+// past |a| of about 87, where t leaves fp32's normal range; r is exactly one
+// where t is nothing against one.  A NaN logit makes both NaN.
 template <typename T>
 __device__ __forceinline__ void gate_rs(uint32_t a, Vf<VRow<T>::CP>& r, Vf<VRow<T>::CP>& s) {
     constexpr int CP = VRow<T>::CP;
@@ -113,7 +115,9 @@ __device__ __forceinline__ void gate_rs(uint32_t a, Vf<VRow<T>::CP>& r, Vf<VRow<
 }
 // The same for two logits with one reciprocal: 1 / (Da Db) gives both (the
 // MUFU unit, at 16 lanes a clock, is what bounds the forward; both
-// denominators lie in [1, 2]).
+// denominators lie in [1, 2]), for two more products in each s.  The larger
+// side is 1 - s here: r Db need not be one where Da is, and a saturated gate
+// has to keep its state bit for bit whatever the other gate is.
 template <typename T>
 __device__ __forceinline__ void gate_rs2(uint32_t a, uint32_t b, Vf<VRow<T>::CP>& ra,
                                          Vf<VRow<T>::CP>& sa, Vf<VRow<T>::CP>& rb,
@@ -127,10 +131,10 @@ __device__ __forceinline__ void gate_rs2(uint32_t a, uint32_t b, Vf<VRow<T>::CP>
     Vf<CP> r = da * db;
 #pragma unroll
     for (int j = 0; j < CP; ++j) r[j] = rcpa_(r[j]);
-    ra = r * db;
-    rb = r * da;
-    sa = ta * ra;
-    sb = tb * rb;
+    sa = ta * (r * db);
+    sb = tb * (r * da);
+#pragma unroll
+    for (int j = 0; j < CP; ++j) ra[j] = 1.0f - sa[j], rb[j] = 1.0f - sb[j];
 }
 // sigmoid(a) of the two sides (with r and s exchanged: 1 - sigmoid(a)).
 template <typename T>

@@ -418,3 +418,24 @@ def test_offsets_past_32_bits():
     for n in ("dh", "da"):
         one, two = tail(grads[n]).float(), grads2[n].float()
         assert float((one - two).abs().max()) <= 2.0 ** -7 * float(two.abs().max()), n
+
+
+@pytest.mark.parametrize("a", [math.inf, 60.0])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_saturated_gate_keeps_the_state(dtype, a):
+    """sigmoid(a) is one to fp32's last place: with h = 0 the state passes any
+    number of tokens bit for bit, whatever the write gate is, in the forward,
+    in steps, and as the adjoint of the backward."""
+    t = make(2, 20000, 64, dtype, z=False, seed=50, b=(0.0, 3.0))
+    t["h"].zero_()
+    t["dy"].zero_()
+    t["a"].fill_(a)
+    t["b"][:, :, 32:] = t["b"][:, :1, 32:]  # half of the channels: one value throughout
+    y, xf, g = run(t, naju.F32)
+    assert torch.equal(xf, t["x0"])
+    assert torch.equal(y, t["x0"][:, None].expand_as(y))
+    assert torch.equal(g["dx0"], t["dx_final"])
+    state = t["x0"].clone()
+    for k in range(20):
+        naju.vscan_step(state, *(t[n][:, k].contiguous() for n in ("h", "a", "b")))
+    assert torch.equal(state, t["x0"])
