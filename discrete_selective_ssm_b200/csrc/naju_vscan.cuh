@@ -228,9 +228,14 @@ __device__ __forceinline__ void send_pair(uint32_t dst, const VPair<2>& v, uint3
         "r"(__float_as_uint(v.X.x.x)), "r"(__float_as_uint(v.X.x.y)), "r"(mbar)
         : "memory");
 }
+// Releases this thread's mbarrier initialisations (and those alone) to the
+// cluster: after the last of them, before cluster_sync.
+__device__ __forceinline__ void mbar_init_release() {
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
 // All blocks of the cluster have come this far.  Relaxed: nothing but the
-// mbarriers' initialisation (fenced by itself) and the right to leave depends
-// on it, so a block does not wait for its stores here.
+// mbarriers' initialisation (released by mbar_init_release) and the right to
+// leave depends on it, so a block does not wait for its stores here.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile(
         "barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
@@ -255,7 +260,6 @@ template <int CP> struct VExchange {
     __device__ __forceinline__ void init() {
         mbar_init(&mbar[0], 1);
         mbar_init(&mbar[1], 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __device__ __forceinline__ void send(int i, uint32_t rank, uint32_t cs, int lane,
                                          const VPair<CP>& v) {

@@ -51,9 +51,10 @@ vscan_bwd_kernel(const __grid_constant__ VscanParams p,
     };
     if (tid == 32 * kVWarps) {
         ex.init();
+        mbar_init(&full, 1);
+        mbar_init(&empty, kVWarps);
+        mbar_init_release();
         if (TMA) {
-            mbar_init(&full, 1);
-            mbar_init(&empty, kVWarps);
             fence_proxy_async();
             if ((int)rank < nk) fetch(rank);
         }
