@@ -6,12 +6,19 @@ checks tensor placement, dtype and contiguity, allocates outputs with torch on t
 passes raw device pointers and the current CUDA stream to the C ABI, and
 raises NajuError on a non-OK status.  All arithmetic runs in the library's
 CUDA kernels; there is no host or PyTorch fallback.
+
+With `stream` a call runs on that stream instead: what it allocates is that
+stream's memory, and every tensor it takes or returns may be dropped at any
+time after the call.  As ever, the given stream has to wait for the work that
+fills the inputs, and a reader of the results for the given stream.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import importlib.machinery
 import importlib.util
+import inspect
 import os
 import re
 import threading
@@ -210,7 +217,48 @@ def alloc_workspace(dims: Dims, device) -> torch.Tensor:
     return ws
 
 
+def _on_given_stream(fn):
+    """fn with its `stream` argument, where one is given, as the current stream
+    meanwhile, so that what fn allocates belongs to it; the allocator holds
+    tensors that one stream owns and the other works on."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        flat = [] if stream is None else _tensors((args, kw))
+        if not flat:
+            return fn(*args, **kw)
+        dev = flat[0].device
+        caller = torch.cuda.current_stream(dev)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream, device=dev)
+        if stream.cuda_stream == caller.cuda_stream:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            out = fn(*args, **kw)
+        for t in flat:
+            t.record_stream(stream)
+        for t in _tensors(out):
+            t.record_stream(caller)
+        return out
+
+    return call
+
+
+def _tensors(v) -> list:
+    """The CUDA tensors in nested tuples and dicts."""
+    if isinstance(v, torch.Tensor):
+        return [v] if v.is_cuda else []
+    if isinstance(v, dict):
+        v = v.values()
+    elif not isinstance(v, (tuple, list)):
+        return []
+    return [t for x in v for t in _tensors(x)]
+
+
 # ------------------------------------------------------------- entry points
+@_on_given_stream
 def conv_silu_fwd(u, conv_w, conv_b=None, out_dtype=None, stream=None):
     Bt, L, d = u.shape
     dims = make_dims(Bt, L, d, 16, _dt(u), out_dtype, conv_w.shape[1])
@@ -222,6 +270,7 @@ def conv_silu_fwd(u, conv_w, conv_b=None, out_dtype=None, stream=None):
     return h
 
 
+@_on_given_stream
 def conv_silu_bwd(u, conv_w, conv_b, dh, stream=None):
     Bt, L, d = u.shape
     dims = make_dims(Bt, L, d, 16, _dt(u), None, conv_w.shape[1])
@@ -236,6 +285,7 @@ def conv_silu_bwd(u, conv_w, conv_b, dh, stream=None):
     return du, dw, db
 
 
+@_on_given_stream
 def scan_fwd(hu, a, b, B, C, *, conv_w=None, conv_b=None, z=None, D=None, x0=None,
              out_dtype=None, workspace=None, want_final=True, y=None, x_final=None,
              stream=None):
@@ -263,6 +313,7 @@ def scan_fwd(hu, a, b, B, C, *, conv_w=None, conv_b=None, z=None, D=None, x0=Non
     return y, x_final, workspace
 
 
+@_on_given_stream
 def scan_bwd(dy, hu, a, b, B, C, workspace, *, conv_w=None, conv_b=None, z=None, D=None,
              x0=None, dx_final=None, out_dtype=None, want_dx0=True, grads=None, stream=None):
     """Gradients of scan_fwd; `workspace` must hold that forward's checkpoints.
@@ -299,6 +350,7 @@ def scan_bwd(dy, hu, a, b, B, C, workspace, *, conv_w=None, conv_b=None, z=None,
     return g
 
 
+@_on_given_stream
 def scan_step(state, h, a, b, B, C, z=None, D=None, y=None, stream=None):
     """One decode step; `state` [Bt, d, N] fp32 is updated in place.  Returns y."""
     Bt, d = h.shape
@@ -312,6 +364,7 @@ def scan_step(state, h, a, b, B, C, z=None, D=None, y=None, stream=None):
     return y
 
 
+@_on_given_stream
 def conv_silu_step(conv_state, u, conv_w, conv_b=None, h=None, stream=None):
     """Decode step of conv + SiLU; `conv_state` [Bt, d, 3] fp32 is updated in
     place (previous three inputs, oldest first).  Returns h."""
@@ -326,6 +379,7 @@ def conv_silu_step(conv_state, u, conv_w, conv_b=None, h=None, stream=None):
     return h
 
 
+@_on_given_stream
 def scan_step_conv(state, conv_state, u, a, b, B, C, conv_w, conv_b=None, z=None, D=None,
                    y=None, stream=None):
     """One decode step from the pre-conv input u (conv + SiLU fused); `state`
@@ -382,6 +436,7 @@ def vscan_step(state, h, a, b=None, z=None, y=None, stream=None):
 
 
 # ------------------------------------------------------ 4-bit projections
+@_on_given_stream
 def w4_quantize(W, group=128, stream=None):
     """Quantises a projection W [n_out, n_in] to 4 bits a weight with one bf16
     scale per `group` (32, 64 or 128) inputs.  Returns (wq, scales): uint8

@@ -6,6 +6,7 @@
 // arithmetic, no kernel: the entry points come as addresses from the loaded
 // libnaju.so.
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -90,16 +91,51 @@ void* ptr(const at::Tensor& t, const char* name, Shape shape, at::ScalarType dt,
 void* ptr(const at::Tensor* t, const char* name, Shape shape, at::ScalarType dt, int dev) {
     return t ? ptr(*t, name, shape, dt, dev) : nullptr;
 }
-// The stream's handle: the device's current one unless given.
-void* stream_of(PyObject* o, int dev) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-    if (!h) throw Raised{};
-    void* s = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
-    if (!s && PyErr_Occurred()) throw Raised{};
-    return s;
-}
+// The device and stream of a call: the device's current stream unless one is
+// given.  A given one is the current one meanwhile, so that what the call
+// allocates is that stream's memory (memory of the caller's stream could still
+// be in use there, and could be handed out again before the kernel has run).
+// Tensors of one stream that the other works on are held by the allocator
+// until that work is done, should they be dropped before.
+class Call {
+public:
+    Call(PyObject* given, int dev)
+        : guard_((c10::DeviceIndex)dev), caller_(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev)),
+          stream_(caller_) {
+        if (given == Py_None) return;
+        PyObject* h = PyObject_GetAttrString(given, "cuda_stream");
+        if (!h) throw Raised{};
+        void* s = PyLong_AsVoidPtr(h);
+        Py_DECREF(h);
+        if (!s && PyErr_Occurred()) throw Raised{};
+        if (s == (void*)cudaStreamLegacy) s = nullptr;
+        if (s == (void*)caller_.stream()) return;
+        stream_ = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), (c10::DeviceIndex)dev);
+        on_.reset_stream(stream_);
+        other_ = true;
+    }
+    void* stream() const { return stream_.stream(); }
+    // An argument that the kernel reads or writes.
+    void uses(const at::Tensor* t) const {
+        if (other_ && t && t->defined()) hold(*t, stream_);
+    }
+    void uses(const at::Tensor& t) const { uses(&t); }
+    // A result that the caller takes back: allocated here, or an argument.
+    void gives(const at::Tensor& t) const {
+        if (!other_ || !t.defined()) return;
+        hold(t, stream_);
+        hold(t, caller_);
+    }
+
+private:
+    static void hold(const at::Tensor& t, c10::cuda::CUDAStream s) {
+        c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), s);
+    }
+    c10::cuda::CUDAGuard guard_;
+    c10::cuda::OptionalCUDAStreamGuard on_;
+    c10::cuda::CUDAStream caller_, stream_;
+    bool other_ = false;
+};
 long long integer(PyObject* o) {
     const long long v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) throw Raised{};
@@ -153,7 +189,7 @@ PyObject* vscan_fwd(PyObject* const* v, Py_ssize_t n) {
     const at::Tensor &a = need(v[1], "a"), *b = opt(v[2], "b"), *z = opt(v[3], "z"),
                      *x0 = opt(v[4], "x0"), *ws0 = opt(v[6], "workspace"), *y0 = opt(v[8], "y"),
                      *xf0 = opt(v[9], "x_final");
-    c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    const Call call(v[10], dev);
     void *ph = ptr(h, "h", act, dt, dev), *pa = ptr(a, "a", act, dt, dev),
          *pb = ptr(b, "b", act, dt, dev), *pz = ptr(z, "z", act, dt, dev);
     void* px0 = ptr(x0, "x0", st, at::kFloat, dev);
@@ -163,8 +199,10 @@ PyObject* vscan_fwd(PyObject* const* v, Py_ssize_t n) {
     const at::Tensor xf = xf0 ? *xf0 : final ? at::empty(st, h.options().dtype(at::kFloat)) : at::Tensor();
     check(g_vscan_fwd(&d, ph, pa, pb, pz, static_cast<float*>(px0), ptr(y, "y", act, ot, dev),
                       final ? static_cast<float*>(ptr(xf, "x_final", st, at::kFloat, dev)) : nullptr,
-                      ws_ptr(ws, dev), (size_t)ws.numel(), stream_of(v[10], dev)),
+                      ws_ptr(ws, dev), (size_t)ws.numel(), call.stream()),
           "naju_vscan_fwd");
+    for (const at::Tensor* t : {&h, &a, b, z, x0}) call.uses(t);
+    for (const at::Tensor* t : {&ws, &y, &xf}) call.gives(*t);
     PyObject* xo = final ? wrap(xf) : Py_NewRef(Py_None);
     return Py_BuildValue("(NNN)", wrap(y), xo, wrap(ws));
 }
@@ -181,7 +219,7 @@ PyObject* vscan_bwd(PyObject* const* v, Py_ssize_t n) {
     const at::Tensor &dy = need(v[0], "dy"), &a = need(v[2], "a"), *b = opt(v[3], "b"),
                      &ws = need(v[4], "workspace"), *z = opt(v[5], "z"),
                      *dxf = opt(v[6], "dx_final");
-    c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    const Call call(v[10], dev);
     void *ph = ptr(h, "h", act, dt, dev), *pa = ptr(a, "a", act, dt, dev),
          *pb = ptr(b, "b", act, dt, dev), *pz = ptr(z, "z", act, dt, dev),
          *pdy = ptr(dy, "dy", act, dt, dev);
@@ -209,8 +247,10 @@ PyObject* vscan_bwd(PyObject* const* v, Py_ssize_t n) {
     };
     check(g_vscan_bwd(&d, ph, pa, pb, pz, pdy, static_cast<float*>(pdxf), out(0), out(1), out(2),
                       out(3), static_cast<float*>(out(4)), ws_ptr(ws, dev), (size_t)ws.numel(),
-                      stream_of(v[10], dev)),
+                      call.stream()),
           "naju_vscan_bwd");
+    for (const at::Tensor* t : {&h, &a, b, z, &dy, dxf, &ws}) call.uses(t);
+    for (const at::Tensor& t : g) call.gives(t);
     if (!own) return Py_NewRef(grads);
     PyObject* r = PyDict_New();
     if (!r) throw Raised{};
@@ -231,13 +271,15 @@ PyObject* vscan_step(PyObject* const* v, Py_ssize_t n) {
     if (sh.size() != 2) raise(PyExc_ValueError, "h must be [batch, d_inner], got " + text(sh));
     const int dev = device_of(h, "h"), code = dtype_of(h);
     const at::ScalarType dt = h.scalar_type();
-    c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    const Call call(v[6], dev);
     const at::Tensor y = y0 ? *y0 : at::empty(sh, h.options());
     check(g_vscan_step(sh[0], sh[1], code, ptr(h, "h", sh, dt, dev), ptr(a, "a", sh, dt, dev),
                        ptr(b, "b", sh, dt, dev), ptr(z, "z", sh, dt, dev),
                        static_cast<float*>(ptr(state, "state", sh, at::kFloat, dev)),
-                       ptr(y, "y", sh, dt, dev), stream_of(v[6], dev)),
+                       ptr(y, "y", sh, dt, dev), call.stream()),
           "naju_vscan_step");
+    for (const at::Tensor* t : {&state, &h, &a, b, z}) call.uses(t);
+    call.gives(y);
     return wrap(y);
 }
 
@@ -257,14 +299,16 @@ PyObject* w4_linear(PyObject* const* v, Py_ssize_t n) {
     c10::DimVector out(x.sizes().begin(), x.sizes().end());
     out.back() = O;
     const int64_t ws[2] = {O, (K + 127) / 128 * 64}, ss[2] = {O, (K + group - 1) / group}, bs[1] = {O};
-    c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    const Call call(v[7], dev);
     void *px = ptr(x, "x", x.sizes(), dt, dev), *pw = ptr(wq, "wq", ws, at::kByte, dev),
          *ps = ptr(sc, "scales", ss, at::kBFloat16, dev);
     void *pb = ptr(bias, "bias", bs, at::kFloat, dev), *pr = ptr(res, "residual", out, dt, dev);
     const at::Tensor y = y0 ? *y0 : at::empty(out, x.options());
     check(g_w4_linear(m, K, O, (int32_t)group, code, px, pw, ps, static_cast<float*>(pb), pr,
-                      ptr(y, "y", out, dt, dev), stream_of(v[7], dev)),
+                      ptr(y, "y", out, dt, dev), call.stream()),
           "naju_w4_linear");
+    for (const at::Tensor* t : {&x, &wq, &sc, bias, res}) call.uses(t);
+    call.gives(y);
     return wrap(y);
 }
 
@@ -274,6 +318,7 @@ struct Cache {
     int8_t* q;
     float* scale;
     int32_t* at;
+    const at::Tensor* given[3];  // the pool's two tensors and the slots
 };
 Cache cache_args(PyObject* pool_q, PyObject* pool_scale, PyObject* slots) {
     const at::Tensor &q = need(pool_q, "pool_q"), &sc = need(pool_scale, "pool_scale"),
@@ -292,6 +337,9 @@ Cache cache_args(PyObject* pool_q, PyObject* pool_scale, PyObject* slots) {
     c.q = static_cast<int8_t*>(ptr(q, "pool_q", q.sizes(), at::kChar, c.dev));
     c.scale = static_cast<float*>(ptr(sc, "pool_scale", ss, at::kFloat, c.dev));
     c.at = static_cast<int32_t*>(ptr(sl, "slots", ls, at::kInt, c.dev));
+    c.given[0] = &q;
+    c.given[1] = &sc;
+    c.given[2] = &sl;
     return c;
 }
 
@@ -300,11 +348,13 @@ PyObject* state_store(PyObject* const* v, Py_ssize_t n) {
     arity(n, 5);
     const at::Tensor& state = need(v[0], "state");
     const Cache c = cache_args(v[2], v[3], v[1]);
-    c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.dev);
+    const Call call(v[4], c.dev);
     check(g_state_store(c.n, c.shape[1], c.shape[2], c.slots,
                         static_cast<float*>(ptr(state, "state", Shape(c.shape, 3), at::kFloat, c.dev)),
-                        c.at, c.q, c.scale, stream_of(v[4], c.dev)),
+                        c.at, c.q, c.scale, call.stream()),
           "naju_state_store");
+    call.uses(state);
+    for (const at::Tensor* t : c.given) call.uses(t);
     Py_RETURN_NONE;
 }
 
@@ -313,14 +363,16 @@ PyObject* state_load(PyObject* const* v, Py_ssize_t n) {
     arity(n, 5);
     const Cache c = cache_args(v[0], v[1], v[2]);
     const at::Tensor* s0 = opt(v[3], "state");
-    c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.dev);
+    const Call call(v[4], c.dev);
     const at::Tensor state = s0 ? *s0
                                 : at::empty(Shape(c.shape, 3),
                                             need(v[1], "pool_scale").options());
     check(g_state_load(c.n, c.shape[1], c.shape[2], c.slots, c.q, c.scale, c.at,
                        static_cast<float*>(ptr(state, "state", Shape(c.shape, 3), at::kFloat, c.dev)),
-                       stream_of(v[4], c.dev)),
+                       call.stream()),
           "naju_state_load");
+    for (const at::Tensor* t : c.given) call.uses(t);
+    call.gives(state);
     return s0 ? Py_NewRef(v[3]) : wrap(state);
 }
 
