@@ -343,6 +343,16 @@ naju_status check_vdims(const naju_dims* dm) {
     return units < (1LL << 26) ? NAJU_OK : NAJU_ERR_INVALID_ARG;
 }
 
+// A number for a forward call's status word: not zero, and another one each
+// time (they come round after 2^32 calls).
+uint32_t next_call() {
+    static std::atomic<uint32_t> n{0};
+    uint32_t v;
+    do v = n.fetch_add(1, std::memory_order_relaxed) + 1;
+    while (v == 0);
+    return v;
+}
+
 void vscan_params(VscanParams& p, const naju_dims* dims, const VLayout& l, char* ws) {
     p.status = reinterpret_cast<int*>(ws);
     p.ckpt = reinterpret_cast<float*>(ws + l.off_ckpt);
@@ -554,6 +564,7 @@ naju_status naju_vscan_fwd(const naju_dims* dims, const void* h, const void* a, 
     vscan_params(p, dims, l, ws);
     p.h = h; p.a = a; p.b = b; p.z = z; p.x0 = x0; p.y = y; p.x_final = x_final;
     p.nk = l.nkf;
+    p.call = next_call();
     p.cluster = vscan_cluster(l.units, l.nkf, 3);
     return cuda_status(launch_vscan_fwd(p, dims->dtype, dims->out_dtype, s));
 }

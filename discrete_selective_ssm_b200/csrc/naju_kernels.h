@@ -168,7 +168,8 @@ struct VscanParams {
     void* db;
     void* dz;
     float* dx0;             // may be null
-    int* status;
+    int* status;            // flags, then the number of their forward call
+    uint32_t call;          // forward: this call's number
     float* ckpt;            // [units][nck][tile]: state at every backward item's start
     int64_t L, d;
     int64_t units, nk;      // batch * channel tiles; this direction's items per unit

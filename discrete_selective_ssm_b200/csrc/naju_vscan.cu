@@ -47,7 +47,6 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
             fence_proxy_async();
             if ((int)rank < nk) fetch(rank);
         }
-        if (blockIdx.x == 0) *p.status = 0;
     }
     __syncwarp();
     if (cs > 1)
@@ -56,6 +55,8 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
         __syncthreads();
 
     if (warp == kVWarps) {  // ------------------------------------- scout
+        const bool first = blockIdx.x == 0 && lane == 0;
+        const StatusWord was = first ? status_begin(p) : 0;
         V E;
         const int64_t row = bb * p.d + c0;
         const int left = (int)min64(W, p.d - c0);
@@ -71,7 +72,7 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
             if (TMA && k + (int)cs < nk) {
                 if (lane == 0) {
                     if (!mbar_wait(&empty, par, kTmaPolls))
-                        atomicOr(p.status, 1 << NAJU_ERR_TIMEOUT);
+                        status_timeout<true>(p);
                     fetch(k + cs);
                 }
                 __syncwarp();
@@ -89,7 +90,7 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
                 ex.send(i, rank, cs, lane, c);
             V mine = E;
             if (cs > 1) {
-                mine = ex.fold(i, rank, cs, lane, E, alive, p.status, p.wait_limit);
+                mine = ex.template fold<true>(i, rank, cs, lane, E, alive, p);
                 sE[par][lane] = mine;
                 named_arrive(2, kVThreads);
             } else {
@@ -108,6 +109,7 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
                 if (ch < left) p.x_final[row + ch] = E[j];
             }
         }
+        if (first) status_keep(p, was);
     } else {  // ------------------------------------------- compute warps
         const int cl = c0 + vchan<CP, VEC>(lane, 0);
         const int left = (int)p.d - cl;
@@ -124,7 +126,7 @@ vscan_fwd_kernel(const __grid_constant__ VscanParams p, const __grid_constant__ 
                 uint32_t rh[RUN], ra[RUN], rb[RUN];
                 if (TMA) {
                     if (!mbar_wait(&full, par, kTmaPolls))
-                        atomicOr(p.status, 1 << NAJU_ERR_TIMEOUT);
+                        status_timeout<true>(p);
                     const unsigned char* at = stage + warp * RUN * 128 + lane * 4;
                     const auto get = [&](int which, int q) {
                         return *reinterpret_cast<const uint32_t*>(at + which * kBox + q * 128);

@@ -91,7 +91,7 @@ vscan_bwd_kernel(const __grid_constant__ VscanParams p,
             if (TMA && o + (int)cs < nk) {
                 if (lane == 0) {
                     if (!mbar_wait(&empty, par, kTmaPolls))
-                        atomicOr(p.status, 1 << NAJU_ERR_TIMEOUT);
+                        status_timeout<false>(p);
                     fetch(o + cs);
                 }
                 __syncwarp();
@@ -108,7 +108,7 @@ vscan_bwd_kernel(const __grid_constant__ VscanParams p,
             if (cs > 1 && alive && !(p.fault_skip_publish && i == 0 && rank == 0))
                 ex.send(i, rank, cs, lane, c);
             if (cs > 1) {
-                sA[par][lane] = ex.fold(i, rank, cs, lane, A, alive, p.status, p.wait_limit);
+                sA[par][lane] = ex.template fold<false>(i, rank, cs, lane, A, alive, p);
                 named_arrive(2, kVThreads);
             } else {
                 A = vfma(c.P, A, c.X);
@@ -141,7 +141,7 @@ vscan_bwd_kernel(const __grid_constant__ VscanParams p,
                 uint32_t rh[RUN], ra[RUN], rb[RUN], rz[RUN], rd[RUN];
                 if (TMA) {
                     if (!mbar_wait(&full, par, kTmaPolls))
-                        atomicOr(p.status, 1 << NAJU_ERR_TIMEOUT);
+                        status_timeout<false>(p);
                     const unsigned char* at = stage + warp * RUN * 128 + lane * 4;
                     const auto get = [&](int which, int q) {
                         return *reinterpret_cast<const uint32_t*>(at + which * kBox + q * 128);

@@ -198,7 +198,8 @@ size_t naju_vscan_workspace_bytes(const naju_dims* dims);
 
 /* Forward over [batch, seqlen, d_inner].  x0 and x_final are [batch, d_inner]
  * fp32; x0 == NULL means zero, x_final may be NULL.  Clears the workspace's
- * status word and writes the checkpoints that the backward reads. */
+ * status word (replays of one captured call keep a timeout that has not been
+ * read yet) and writes the checkpoints that the backward reads. */
 naju_status naju_vscan_fwd(const naju_dims* dims, const void* h, const void* a, const void* b,
                            const void* z, const float* x0, void* y, float* x_final,
                            void* workspace, size_t workspace_bytes, void* stream);

@@ -31,3 +31,13 @@ def test_every_initialisation_is_released(name):
     assert names == ["full", "empty"] and len(inits) == len(names) + 1
     first_sync = text.index("cluster_sync()")
     assert max(inits) < release < first_sync
+
+
+@pytest.mark.parametrize("name", ["naju_vscan.cu", "naju_vscan_bwd.cu", "naju_vscan.cuh"])
+def test_the_status_word_changes_by_atomics_alone(name):
+    """A plain store of one block could undo the timeout that another, which
+    nothing orders after it, has recorded."""
+    text = source(name)
+    for m in re.finditer(r"\bp\.status\b", text):
+        assert re.search(r"(status_timeout_of\(|atomicOr\(|reinterpret_cast<StatusWord\*>\()$",
+                         text[:m.start()]), text[m.start() - 40:m.end() + 20]
