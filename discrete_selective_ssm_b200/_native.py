@@ -136,7 +136,9 @@ def _load_bind():
     L = lib()
     with _lock:
         if _bind is None:
-            path = _build.BIND if os.path.exists(_build.BIND) else _build.build_bind()
+            path = _build.bind_path()
+            if not os.path.exists(path):
+                path = _build.build_bind()
             loader = importlib.machinery.ExtensionFileLoader("_naju_bind", path)
             spec = importlib.util.spec_from_file_location("_naju_bind", path, loader=loader)
             mod = importlib.util.module_from_spec(spec)

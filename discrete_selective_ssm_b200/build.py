@@ -6,13 +6,16 @@ nvcc compiles every ``csrc/*.cu`` to an object file (in parallel, under
 ``_build/`` at the repository root) and links them into one shared library
 next to this file; the build is skipped when the library is newer than all
 sources and headers, and an object is recompiled only when it is older than
-its source or any header.  g++ compiles ``csrc/naju_bind.cpp``, the compiled
-part of the Python binding, against the installed torch.
+its source or any header.  That needs nvcc alone: the C ABI has no part of
+Python in it.  ``build_bind`` compiles ``csrc/naju_bind.cpp``, the compiled
+part of the Python binding, with g++ against the running Python and the
+installed torch, whose names the file carries.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -25,7 +28,6 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libnaju.so")
-BIND = os.path.join(HERE, "_naju_bind.so")
 BIND_SRC = os.path.join(CSRC, "naju_bind.cpp")
 OBJDIR = os.path.join(ROOT, "_build")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -75,15 +77,23 @@ def _compile(src: str, force: bool, verbose: bool) -> str:
     return obj
 
 
+def bind_path() -> str:
+    """Where the compiled part of the Python binding is kept: one file for each
+    Python ABI and torch version, since it is of use to those alone."""
+    torch = importlib.metadata.version("torch")
+    return os.path.join(HERE, f"_naju_bind.{sysconfig.get_config_var('SOABI')}.torch{torch}.so")
+
+
 def build_bind(force: bool = False, verbose: bool = False) -> str:
     """The compiled part of the Python binding (an extension module)."""
+    bind = bind_path()
     deps = [BIND_SRC, os.path.join(INCLUDE, "naju.h")]
-    if not force and os.path.exists(BIND) and all(
-            os.path.getmtime(f) <= os.path.getmtime(BIND) for f in deps):
-        return BIND
+    if not force and os.path.exists(bind) and all(
+            os.path.getmtime(f) <= os.path.getmtime(bind) for f in deps):
+        return bind
     torch = importlib.util.find_spec("torch").submodule_search_locations[0]
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
-    tmp = BIND + f".tmp{os.getpid()}"
+    tmp = bind + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE,
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
            "-I", os.path.join(torch, "include"),
@@ -93,12 +103,11 @@ def build_bind(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
-    os.replace(tmp, BIND)
-    return BIND
+    os.replace(tmp, bind)
+    return bind
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    build_bind(force, verbose)
     if not force and not _stale():
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)
@@ -115,5 +124,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    build(force="--force" in sys.argv, verbose="-v" in sys.argv)
-    print(LIB)
+    how = {"force": "--force" in sys.argv, "verbose": "-v" in sys.argv}
+    print(build(**how), flush=True)
+    if importlib.util.find_spec("torch") is not None:
+        print(build_bind(**how))
