@@ -164,6 +164,7 @@ class NajuBlock:
         """One token x [batch, d_model] of every session; `state` (new_state or
         prefill) is updated in place.  Returns the block's output."""
         p, dt, di = self.p, self.dtype, self.d_inner
+        x = x.contiguous()  # (tokens of a prompt, x[:, t], are strided)
         xf = x.float()
         r = torch.rsqrt(xf.pow(2).mean(-1, keepdim=True) + EPS)
         uz = self._project("W_in", (xf * r * p["norm_w"]).to(dt))

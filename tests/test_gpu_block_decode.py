@@ -194,3 +194,20 @@ def test_a_wider_residual_keeps_its_bits():
         if not quantised:
             assert_close(y, out[:, 0].cpu().numpy(), 1e-2, name="out")
         assert np.abs(added).max() > 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N", [1, 16])
+def test_steps_take_strided_tokens(N, dtype):
+    """Tokens cut out of a prompt, and with the batch as the inner dimension,
+    on the full and on the 4-bit projections."""
+    blk = NajuBlock(64, 128, N, "cuda", dtype=dtype, seed=11)
+    x = torch.randn(3, 5, 64, generator=torch.Generator().manual_seed(12)).to(dtype).cuda()
+    for quantised in (False, True):
+        if quantised:
+            blk.quantize(group=32)
+        want = blk.step(x[:, 2].contiguous(), blk.new_state(3))
+        assert not x[:, 2].is_contiguous()
+        assert torch.equal(blk.step(x[:, 2], blk.new_state(3)), want)
+        inner = x[:, 2].t().contiguous().t()
+        assert torch.equal(blk.step(inner, blk.new_state(3)), want)
