@@ -141,6 +141,11 @@ long long integer(PyObject* o) {
     if (v == -1 && PyErr_Occurred()) throw Raised{};
     return v;
 }
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Raised{};
+    return v != 0;
+}
 PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
 void arity(Py_ssize_t n, Py_ssize_t want) {
     if (n != want) raise(PyExc_TypeError, "wrong number of arguments");
@@ -195,7 +200,7 @@ PyObject* vscan_fwd(PyObject* const* v, Py_ssize_t n) {
     void* px0 = ptr(x0, "x0", st, at::kFloat, dev);
     const at::Tensor ws = ws0 ? *ws0 : workspace(d, h);
     const at::Tensor y = y0 ? *y0 : at::empty(act, h.options().dtype(ot));
-    const bool final = xf0 || PyObject_IsTrue(v[7]) == 1;
+    const bool final = xf0 || truth(v[7]);
     const at::Tensor xf = xf0 ? *xf0 : final ? at::empty(st, h.options().dtype(at::kFloat)) : at::Tensor();
     check(g_vscan_fwd(&d, ph, pa, pb, pz, static_cast<float*>(px0), ptr(y, "y", act, ot, dev),
                       final ? static_cast<float*>(ptr(xf, "x_final", st, at::kFloat, dev)) : nullptr,
@@ -231,7 +236,7 @@ PyObject* vscan_bwd(PyObject* const* v, Py_ssize_t n) {
     for (int i = 0; i < 5; ++i) {
         if (own) {
             const bool want = i < 2 || (i == 2 && b) || (i == 3 && z) ||
-                              (i == 4 && PyObject_IsTrue(v[8]) == 1);
+                              (i == 4 && truth(v[8]));
             if (!want) continue;
             g[i] = i == 4 ? at::empty(st, h.options().dtype(at::kFloat))
                           : at::empty(act, h.options().dtype(ot));

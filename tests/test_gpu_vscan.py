@@ -439,3 +439,13 @@ def test_a_saturated_gate_keeps_the_state(dtype, a):
     for k in range(20):
         naju.vscan_step(state, *(t[n][:, k].contiguous() for n in ("h", "a", "b")))
     assert torch.equal(state, t["x0"])
+
+
+def test_a_flag_without_a_truth_value_is_refused():
+    t = make(1, 10, 32, "f32")
+    neither = torch.ones(2)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        naju.vscan_fwd(t["h"], t["a"], want_final=neither)
+    _, _, ws = naju.vscan_fwd(t["h"], t["a"])
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        naju.vscan_bwd(t["dy"], t["h"], t["a"], None, ws, want_dx0=neither)
