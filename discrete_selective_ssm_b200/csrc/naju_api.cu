@@ -306,6 +306,10 @@ inline naju_status cuda_status(cudaError_t e) { return e == cudaSuccess ? NAJU_O
 
 inline bool ok_act(const void* p) { return p && aligned(p, 16); }
 inline bool ok_opt(const void* p) { return !p || aligned(p, 16); }
+inline bool apart(const void* p, int64_t bytes, const void* q, int64_t q_bytes) {
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+    return !p || !q || a + (uintptr_t)bytes <= b || b + (uintptr_t)q_bytes <= a;
+}
 
 }  // namespace
 
@@ -628,7 +632,13 @@ naju_status naju_w4_linear(int64_t m, int64_t n_in, int64_t n_out, int32_t group
     if (st != NAJU_OK) return st;
     NAJU_REQUIRE(m >= 1 && m <= (1 << 20));
     NAJU_REQUIRE(ok_act(x) && ok_act(wq) && scales && aligned(scales, 2) && ok_act(y));
-    NAJU_REQUIRE(ok_opt(residual) && (!bias || aligned(bias, 4)) && y != x);
+    NAJU_REQUIRE(ok_opt(residual) && (!bias || aligned(bias, 4)));
+    // y over anything that other blocks still read (residual: but for its own place)
+    const int64_t e = dtype == NAJU_F32 ? 4 : 2, out = m * n_out * e;
+    NAJU_REQUIRE(apart(y, out, x, m * n_in * e) && apart(y, out, bias, 4 * n_out) &&
+                 (residual == y || apart(y, out, residual, out)) &&
+                 apart(y, out, wq, n_out * cdiv(n_in, 128) * 64) &&
+                 apart(y, out, scales, 2 * n_out * cdiv(n_in, group)));
     return cuda_status(launch_w4_linear(m, n_in, n_out, group, dtype, x, wq, scales, bias,
                                         residual, y, g_w4_impl, sm_count(),
                                         static_cast<cudaStream_t>(stream)));

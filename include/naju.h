@@ -238,7 +238,7 @@ naju_status naju_w4_quantize(int64_t n_out, int64_t n_in, int32_t group, int32_t
 
 /* y = x W^T (+ bias) (+ residual): x [m, n_in], y and residual [m, n_out] in
  * `dtype`, bias [n_out] fp32; bias and residual may be NULL; residual may be
- * y itself, x may not (INVALID_ARG).  Sums are fp32 and every product is exact (bf16 x) or exact to
+ * y itself, but y may overlap no input in any other way (INVALID_ARG).  Sums are fp32 and every product is exact (bf16 x) or exact to
  * 2^-24 of it (fp32 x); y is rounded once.  m is at most 2^20, but the
  * weights are read again for every 64 rows of x: meant for m up to a few
  * hundred.  Uses no workspace; a bounded wait inside that runs out shows as

@@ -132,3 +132,21 @@ def test_w4_binding_refusals():
     with pytest.raises(ValueError):
         naju.w4_linear(torch.zeros(1, 64), torch.zeros(8, 64, dtype=torch.uint8),
                        torch.zeros(8, 1, dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("dtype,e", [(naju.F32, 4), (naju.BF16, 2)])
+def test_w4_results_over_inputs_are_refused(L, dtype, e):
+    """y anywhere over an input, but for the residual's own place."""
+    m, K, O, G = 3, 256, 64, 32
+    p = lambda v: ctypes.c_void_p(v)  # noqa: E731
+    names = ("x", "wq", "scales", "bias", "residual")
+    size = dict(x=m * K * e, wq=O * K // 2, scales=2 * O * K // G, bias=4 * O, residual=m * O * e)
+    at = {n: (1 << 20) * (i + 1) for i, n in enumerate(names)}
+    out = m * O * e
+    f = lambda y: L.naju_w4_linear(m, K, O, G, dtype, *(p(at[n]) for n in names), p(y), None)  # noqa: E731
+    for n in names:
+        for y in (at[n] + 16, at[n] - 16, at[n] + size[n] - 16, at[n] - out + 16):
+            assert f(y) == 1, (n, y - at[n])
+    for n in names:
+        if n != "residual":
+            assert f(at[n]) == 1, n
