@@ -23,8 +23,11 @@
 // next item's tiles brought in by TMA as soon as the compute warps have read
 // the present one's.  Measured against items taken from a ticket with a
 // look-back through global flags (16 x 4096 x 2048 bf16 / 1 x 65536 x 2048):
-// forward 305 / 803 us there, 252 / 351 us here (5.3 and 3.8 TB/s); backward
-// 1031 / 2231 and 570 / 600 us (4.2 and 4.0 TB/s).
+// forward 305 / 803 us there, 252 / 352 us here (5.3 and 3.8 TB/s); backward
+// 1031 / 2231 and 564 / 592 us (4.3 and 4.1 TB/s).  What bounds them is the
+// latency of a round (barriers, exchange, tile wait) with the warps that fit:
+// issue slots are 51 and 49 % busy, no unit more than half (the forward's
+// MUFU 48 %), HBM 38 and 39 % on 4 x 2048 x 2048.
 #pragma once
 #include "naju_common.cuh"
 #include "naju_kernels.h"
@@ -114,8 +117,8 @@ __device__ __forceinline__ void gate_rs(uint32_t a, Vf<VRow<T>::CP>& r, Vf<VRow<
     s = t * r;
 }
 // The same for two logits with one reciprocal: 1 / (Da Db) gives both (the
-// MUFU unit, at 16 lanes a clock, is what bounds the forward; both
-// denominators lie in [1, 2]), for two more products in each s.  The larger
+// MUFU unit, at 16 lanes a clock, is the forward's busiest; both denominators
+// lie in [1, 2]), for two more products in each s.  The larger
 // side is 1 - s here: r Db need not be one where Da is, and a saturated gate
 // has to keep its state bit for bit whatever the other gate is.
 template <typename T>

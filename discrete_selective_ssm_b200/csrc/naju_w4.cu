@@ -26,7 +26,9 @@ namespace naju {
 
 // -------------------------------------------------------------- quantiser
 // One warp per (row, 128-input block); lane l handles inputs 4 l .. 4 l + 3
-// and a group's maximum is taken over G / 4 lanes.
+// and a group's maximum is taken over G / 4 lanes.  Runs once per weight, as
+// weights are laid out: 28672 x 8192 bf16 668 us (its bytes alone: 92), from
+// scalar loads and a division for every weight.
 template <typename T>
 __global__ void __launch_bounds__(128)
 w4_quantize_kernel(int64_t n_out, int64_t n_in, int group, const T* __restrict__ W,
@@ -319,9 +321,14 @@ __global__ void __launch_bounds__(256) w4_linear_kernel(const W4Params p) {
 // exactly; the 16^-i (and the 1 / 1024 of unpack_pair) is in the x that is
 // staged.  A word's eight products are summed unscaled and enter the row's sum
 // with its group's scale.
-// About 30 instructions for eight weights: 1 x 8192 -> 28672 bf16 45 us (2.7
-// TB/s; a plain sum over the same bytes takes 27.6), 1 x 1024 -> 4096 2.8 us.
-// Two rows a warp 50 us, eight 52, two resident blocks 49.
+// 28 instructions for eight weights: 1 x 8192 -> 28672 bf16 45 to 46 us (2.7
+// TB/s; a plain sum over the same bytes takes 27.6), 1 x 1024 -> 4096 3.0 us.
+// No unit is full (issue slots 60 %, logic and shifts 55 %, HBM 32 %); the
+// warps wait for weights most often.  Two rows a warp 50 us, eight 52, two
+// resident blocks 49: three were chosen on this form (groups of 128, one row
+// of x), whose 78 registers they allow without a spill.  Groups of 64 and 32
+// and two rows of x spill 32 to 220 bytes there: 47, 54 and (groups of 128 /
+// 32) 65, 94 us; two resident blocks were not timed for those.
 constexpr int kR = 4;           // rows of W per warp
 constexpr int kRowsSlices = 8;  // slices of x in shared memory at a time
 
@@ -508,7 +515,7 @@ static cudaError_t w4_run(W4Params p, int sms, cudaStream_t st) {
 template <typename T, int G>
 static cudaError_t w4_pick(const W4Params& p, int impl, int sms, cudaStream_t st) {
     // One or two rows: CUDA cores (1 x 8192 -> 28672 bf16: 45 us, against 61 for
-    // the warp-level tensor-core form; 1 x 1024 -> 4096: 2.8 and 4.2 us).
+    // the warp-level tensor-core form; 1 x 1024 -> 4096: 3.0 and 4.2 us).
     if (impl == 0 && p.m == 1) return w4_rows<T, G, 1>(p, sms, st);
     if (impl == 0 && p.m == 2) return w4_rows<T, G, 2>(p, sms, st);
     // tcgen05 from about 2^28 products on (x in whole tiles of 8 rows): its

@@ -15,9 +15,11 @@
 // So every product and every sum is exact or fp32, as in the warp-level kernel.
 // The blocks of a cluster share the inputs and add their sums through
 // distributed shared memory in fixed order.
-// Bound by the hand-over between the warps (a 128 x 128 block of weights takes
-// about 1.9 K cycles, of which issuing its eight products 560): 256 x 2048 ->
-// 4096 17 us, 64 x 8192 -> 28672 62 us (235 us in the warp-level form).
+// Bound by the hand-over between the warps, which wait for tensor memory and
+// for one another (issue slots 38 to 44 % busy, tensor pipe 13 and 24 %):
+// 256 x 2048 -> 4096 17.5 us in groups of 64, 64 x 8192 -> 28672 63 us (235 us
+// in the warp-level form).  Groups of 32 with 64 rows of x spill 212 bytes:
+// 256 x 2048 -> 4096 28 us.
 #include <cooperative_groups.h>
 
 #include "naju_common.cuh"

@@ -190,7 +190,8 @@ naju_status naju_scan_step_conv(int64_t batch, int64_t d_inner, int64_t d_state,
  * The gates saturate exactly: a = -inf starts a sequence afresh at that token
  * (packed documents), a = +inf with b = -inf leaves the state as it is
  * (padding); h and z must be finite there.  Results do not depend on how the
- * work was scheduled: two calls on the same inputs agree bit for bit. */
+ * work was scheduled: two calls on the same inputs agree bit for bit.  Outputs
+ * may overlap neither inputs nor one another. */
 
 /* Workspace of naju_vscan_fwd / naju_vscan_bwd, under the rules of
  * naju_scan_workspace_bytes; it need not be cleared.  0 if dims are invalid. */
@@ -238,11 +239,12 @@ naju_status naju_w4_quantize(int64_t n_out, int64_t n_in, int32_t group, int32_t
 
 /* y = x W^T (+ bias) (+ residual): x [m, n_in], y and residual [m, n_out] in
  * `dtype`, bias [n_out] fp32; bias and residual may be NULL; residual may be
- * y itself, but y may overlap no input in any other way (INVALID_ARG).  Sums are fp32 and every product is exact (bf16 x) or exact to
- * 2^-24 of it (fp32 x); y is rounded once.  m is at most 2^20, but the
- * weights are read again for every 64 rows of x: meant for m up to a few
- * hundred.  Uses no workspace; a bounded wait inside that runs out shows as
- * NaN in the outputs. */
+ * y itself, but y may overlap no input in any other way (INVALID_ARG).  Sums
+ * are fp32 and every product is exact (bf16 x) or exact to 2^-24 of it (fp32
+ * x) for |x| above 2^-100, below which x loses places; y is rounded once.  m is
+ * at most 2^20, but the weights are read again for every 64 rows of x: meant
+ * for m up to a few hundred.  Uses no workspace; a bounded wait inside that
+ * runs out shows as NaN in the outputs. */
 naju_status naju_w4_linear(int64_t m, int64_t n_in, int64_t n_out, int32_t group, int32_t dtype,
                            const void* x, const void* wq, const void* scales, const float* bias,
                            const void* residual, void* y, void* stream);

@@ -131,7 +131,7 @@ def test_no_initial_state_and_no_final_gradient():
 
 
 def test_one_long_sequence():
-    """Many items of one unit: the look-back spans more than its window."""
+    """Many items of one unit: many rounds of a full cluster."""
     check(make(1, 20000, 40, "f32", seed=9))
 
 

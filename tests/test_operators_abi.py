@@ -24,7 +24,7 @@ def test_vscan_workspace(L):
     dm = dims(2, 300, 200)
     n = L.naju_vscan_workspace_bytes(ctypes.byref(dm))
     assert n % 256 == 0 and n >= 2 * 5 * 200 * 4
-    # one item per unit needs no flags and no aggregates
+    # (the status word and one item's checkpoints per unit)
     assert L.naju_vscan_workspace_bytes(ctypes.byref(dims(2, 32, 200))) < 8192
     for bad in (dims(N=16), dims(Bt=0), dims(seq=0), dims(d=0), dims(dtype=7),
                 dims(out=naju.BF16), dims(1 << 20, 1 << 26, 1)):
