@@ -449,3 +449,34 @@ def test_a_flag_without_a_truth_value_is_refused():
     _, _, ws = naju.vscan_fwd(t["h"], t["a"])
     with pytest.raises(RuntimeError, match="ambiguous"):
         naju.vscan_bwd(t["dy"], t["h"], t["a"], None, ws, want_dx0=neither)
+
+
+@pytest.mark.parametrize("coupled", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_each_gate_by_itself(dtype, coupled):
+    """One token from a state of one with nothing written leaves f, from no
+    state with h = 1 the write gate.  The smaller side s of a gate is off by
+    at most (1.5 |a| + 10) u of itself (constant and argument of the
+    exponential |a| u and 0.3 |a| u, the exponential 2^-22.5, sum u, reciprocal
+    2 u, three products), the larger by that of s and half a place below one
+    (2^-25); a coupled gate of bf16 logits takes the reciprocal itself (2 u)."""
+    n = 8192
+    a = torch.linspace(-30.0, 30.0, n).to(DT[dtype]).cuda().view(1, 1, n)
+    b = a.flip(-1).contiguous()
+    zero, one = torch.zeros_like(a), torch.ones_like(a)
+    x1 = torch.ones(1, n, device="cuda")
+    write = -a if coupled else b
+    half = 2 * U if coupled and dtype == "bf16" else U / 2
+    for h, x0, logit in ((zero, x1, a), (one, None, write)):
+        _, got, _ = naju.vscan_fwd(h, a, None if coupled else b, x0=x0)
+        v = ref.f64(logit).reshape(n)
+        s = ref.sigmoid(-np.abs(v))
+        allow = s * (1.5 * np.abs(v) + 10) * U + np.where(v >= 0, half, 0.0)
+        err = np.abs(ref.f64(got).reshape(n) - ref.sigmoid(v))
+        k = int(np.argmax(err - allow))
+        assert err[k] <= allow[k], f"logit {v[k]}: off by {err[k] / U:.2f} u, allowed {allow[k] / U:.2f} u"
+    state = x1.clone()
+    naju.vscan_step(state, zero[0], a[0], None if coupled else b[0])
+    v = ref.f64(a).reshape(n)
+    allow = ref.sigmoid(-np.abs(v)) * (1.5 * np.abs(v) + 10) * U + np.where(v >= 0, U / 2, 0.0)
+    assert (np.abs(ref.f64(state).reshape(n) - ref.sigmoid(v)) <= allow).all()
