@@ -105,10 +105,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 // in a base-2 exponential, its two steps, sum, reciprocal, product) and zero
 // past |a| of about 87, where t leaves fp32's normal range; r is exactly one
 // where t is nothing against one.  For fp32 logits r is 1 - s instead: half a
-// rounding where the sum and the reciprocal make up to two, which a state that
-// sums 150 tokens feels (8 x 512 x 192: 4.8e-7 off, so 2.1e-7; without z it
-// costs 161 -> 167 us on 16 x 4096 x 1024, with z nothing; bf16 would pay 4 %
-// for what its results round away).  A NaN logit makes both NaN.
+// rounding where the sum and the reciprocal make up to two, which shows in a
+// state that sums 150 tokens (8 x 512 x 192: 2.2e-7 from 64 bits instead of
+// 4.8e-7; 16 x 4096 x 1024 without z 161 -> 167 us, with z the same).  With
+// bf16 logits it would cost 4 % for what the results' rounding hides.  A NaN
+// logit makes both NaN.
 template <typename T>
 __device__ __forceinline__ void gate_rs(uint32_t a, Vf<VRow<T>::CP>& r, Vf<VRow<T>::CP>& s) {
     constexpr int CP = VRow<T>::CP;

@@ -130,3 +130,22 @@ def test_the_current_stream_given():
     assert torch.equal(naju.vscan_fwd(h, a, stream=torch.cuda.current_stream())[0], y)
     with pytest.raises(AttributeError):
         naju.vscan_fwd(h, a, stream=3)
+
+
+def test_the_default_stream_given_on_another():
+    """The default stream's handle is zero."""
+    h, a = rn(1, 100, 64), rn(1, 100, 64, mean=5.0)
+    state, row = rn(4, 64), rn(4, 64, seed=1)
+    w = rn(64, 128)
+    y, (wq, sc) = naju.vscan_fwd(h, a)[0], naju.w4_quantize(w)
+    step = naju.vscan_step(state.clone(), row, row)
+    torch.cuda.synchronize()
+    default = torch.cuda.default_stream()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = naju.vscan_fwd(h, a, stream=default)[0]
+        got_wq, got_sc = naju.w4_quantize(w, stream=default)
+        got_step = naju.vscan_step(state, row, row, stream=torch.cuda.ExternalStream(0))
+        torch.cuda.current_stream().wait_stream(default)
+        assert torch.equal(got, y) and torch.equal(got_wq, wq) and torch.equal(got_sc, sc)
+        assert torch.equal(got_step, step)
+    torch.cuda.synchronize()
